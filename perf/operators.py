@@ -336,7 +336,9 @@ def _plain_store(s):
             pool[at, :, slot] = x.half()
             out.append(pool)
         else:
-            d = x.abs().amax(-1, keepdim=True) / 127
+            # (divided by a tensor: a plain 127 would be a product with its rounded reciprocal)
+            top = x.abs().amax(-1, keepdim=True)
+            d = top / torch.full_like(top, 127)
             q = torch.where(d > 0, torch.round(x / d), torch.zeros_like(x))
             pool[at, :, slot] = q.to(torch.int8)
             s[p + "s"][at, :, slot] = d[..., 0]
