@@ -1,0 +1,563 @@
+// attn_impl.h - attention of one new token per sequence over a paged
+// key-value cache (gfx950).
+//
+// For query head h of a sequence, over the tokens t that it sees:
+//   z_t = scale * q_h . K_t,   y_h = sum_t exp(z_t) V_t / sum_t exp(z_t)
+// in one pass with a running maximum m: p_t = 2^(z_t log2(e) - m), and what
+// was summed before is multiplied by 2^(m_old - m_new) when m rises.
+//
+// The matrix cores do both products.  A wave takes 32 tokens (two sub-tiles
+// of 16) and up to 16 query heads that share the key-value head:
+//   S^T (tokens x heads) = K Q^T,  O^T (dims x heads) += V^T P^T,
+// with v_mfma_f32_16x16x32_f16.  The result of the first has in lane
+// (g = lane / 16, j = lane % 16) head j and tokens 4g..4g+3 of each sub-tile,
+// which is the second's right operand as it stands (the order of the summed
+// tokens is free as long as V uses the same), so the probabilities never
+// leave their registers.  V is read row by row, lane (g, j) taking dims
+// j*D/16 .. of its eight tokens, and a byte permute pairs tokens into the
+// left operand.  All of a lane's softmax state belongs to its head j.
+//
+// fp16 keys and values are exact operands.  q and p are not: each is split
+// into a high and a low fp16 part (two products, about 22 bits), q scaled by
+// a power of two to a largest magnitude of 2^13..2^14 and p by 2^14, so that
+// the parts' absolute precision is 2^-38 of the largest.  8-bit keys and
+// values are whole numbers, exact in fp16; the key's scale multiplies z, the
+// value's multiplies p (relative to the largest met so far).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "attn.h"
+#include "qk_common.h"
+#include "qk_internal.h"
+
+namespace qk {
+
+typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
+typedef float f4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
+
+constexpr float kAttnLow = -3.402823466e38f;  // the running maximum before any token
+constexpr float kAttnPexp = 14.0f;            // probabilities are held times 2^14
+
+// Largest / sum of the four lanes that share lane % 16, to all of them.
+__device__ __forceinline__ float quad_rows_max(float v) {
+    u2_t r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    v = fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+    r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+__device__ __forceinline__ float quad_rows_sum(float v) {
+    u2_t r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    v = __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+    r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+
+// High and low fp16 parts of eight values (both rounded toward zero, one
+// instruction for two values; the low part takes up the high part's error,
+// which leaves 2^-21 of the value).
+__device__ __forceinline__ void split8(const float (&p)[8], h8_t &hi, h8_t &lo) {
+    u4_t h, l;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const h2_t a = __builtin_bit_cast(h2_t, __builtin_amdgcn_cvt_pkrtz(p[2 * i], p[2 * i + 1]));
+        h[i] = __builtin_bit_cast(uint32_t, a);
+        l[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(p[2 * i] - (float)a[0], p[2 * i + 1] - (float)a[1]));
+    }
+    hi = __builtin_bit_cast(h8_t, h);
+    lo = __builtin_bit_cast(h8_t, l);
+}
+
+// Two bytes b, held as code + 128 in the low halves of a dword's 16-bit words
+// (fp16 subnormals b * 2^-24), to fp16 code * 2^-9: exact.
+__device__ __forceinline__ uint32_t codes_f16(uint32_t w) {
+    const h2_t x = __builtin_bit_cast(h2_t, w);
+    const h2_t c = {(_Float16)32768.0f, (_Float16)32768.0f};
+    const h2_t o = {(_Float16)-0.25f, (_Float16)-0.25f};
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(x, c, o));
+}
+constexpr float kCodeUnit = 512.0f;  // 2^9
+
+// Eight int8 codes to fp16 code * 2^-9.
+__device__ __forceinline__ h8_t codes8_f16(uint32_t w0, uint32_t w1) {
+    w0 ^= 0x80808080u;
+    w1 ^= 0x80808080u;
+    const u4_t x = {codes_f16(__builtin_amdgcn_perm(0u, w0, 0x0c010c00u)), codes_f16(__builtin_amdgcn_perm(0u, w0, 0x0c030c02u)),
+                    codes_f16(__builtin_amdgcn_perm(0u, w1, 0x0c010c00u)), codes_f16(__builtin_amdgcn_perm(0u, w1, 0x0c030c02u))};
+    return __builtin_bit_cast(h8_t, x);
+}
+
+template <int N> struct Bytes { uint32_t w[(N + 3) / 4]; };
+
+template <int N>
+__device__ __forceinline__ Bytes<N> load_bytes(const uint8_t *p) {
+    Bytes<N> r;
+    if constexpr (N % 4 != 0) r.w[N / 4] = 0;
+    __builtin_memcpy(r.w, p, N);
+    return r;
+}
+
+// TILED: a page holds whole sub-tiles (page_size a multiple of 16) and scales
+// of neighbouring tokens lie side by side, so a sub-tile's page is looked up
+// once, in scalar registers; otherwise every lane looks up its own tokens.
+template <int D, bool I8, bool TILED>
+__global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode_kernel(const AttnArgs a) {
+    constexpr int ES = I8 ? 1 : 2;         // bytes of a key or value element
+    constexpr int STEPS = D / 32;          // products over the head dimension
+    constexpr int DPL = D / 16;            // dims of a lane's V row piece = tiles of O^T
+    constexpr int VB = DPL * ES;           // its bytes
+    constexpr int KP = I8 ? (STEPS + 1) / 2 : STEPS;  // 16-byte pieces of a lane's K row part
+    __shared__ float sm[kAttnWaves][kAttnHeads][2];
+    __shared__ __attribute__((aligned(16))) float so[kAttnWaves][kAttnHeads][D + 4];
+
+    typedef const __attribute__((address_space(4))) int32_t cint_t;  // scalar loads
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = lane >> 4, j = lane & 15;
+    int b = blockIdx.x;
+    const int chunk = b % a.nchunks;
+    b /= a.nchunks;
+    const int ht = b % a.head_tiles;
+    b /= a.head_tiles;
+    const int kvh = b % a.n_kv;
+    const int seq = b / a.n_kv;
+
+    const int len_in = *(cint_t *)(uintptr_t)(a.lens + seq);
+    const bool too_long = len_in > a.max_len;
+    const AttnSpan sp = attn_span(len_in < 0 ? 0 : too_long ? 0 : len_in, a.window, a.sinks);
+    const int head0 = kvh * a.group + ht * kAttnHeads;
+    const int nh = min(kAttnHeads, a.group - ht * kAttnHeads);
+    if (sp.tiles == 0) {
+        // no token to see: zeros (NaN where the length is past max_len)
+        if (chunk == 0) {
+            const float z = too_long ? __builtin_nanf("") : 0.0f;
+            for (int i = threadIdx.x; i < nh * D; i += 64 * kAttnWaves) {
+                const int64_t at = seq * a.y_seq + (head0 + i / D) * a.y_head + i % D;
+                if (a.out_f16) static_cast<uint16_t *>(a.y)[at] = f2h(z);
+                else static_cast<float *>(a.y)[at] = z;
+            }
+        }
+        return;
+    }
+    const int tbeg = chunk * a.chunk_tiles;
+    const int tend = min(tbeg + a.chunk_tiles, sp.tiles);
+    if (tbeg >= tend) return;  // (whole workgroup, before any barrier)
+
+    // q: lane (g, j) holds head j, the dims that its K pieces hold
+    auto dim_of = [&](int s) {  // first of step s's eight dims in this lane
+        if constexpr (I8) {
+            if (STEPS % 2 == 1 && s == STEPS - 1) return 32 * s + 8 * g;
+            return 64 * (s >> 1) + 16 * g + 8 * (s & 1);
+        } else {
+            return 32 * s + 8 * g;
+        }
+    };
+    h8_t qh[STEPS], ql[STEPS];
+    int qexp = 0;
+    {
+        const float *q = a.q + seq * a.q_seq + (int64_t)(head0 + min(j, nh - 1)) * a.q_head;
+        float qv[STEPS][8], top = 0.0f;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            __builtin_memcpy(qv[s], q + dim_of(s), 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                qv[s][i] *= a.qscale;
+                top = fmaxf(top, fabsf(qv[s][i]));
+            }
+        }
+        top = quad_rows_max(top);
+        int ex = 14;
+        if (top > 0.0f && top <= 3.402823466e38f) (void)frexpf(top, &ex);
+        qexp = ex - 14;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) qv[s][i] = ldexpf(qv[s][i], -qexp);
+            split8(qv[s], qh[s], ql[s]);
+        }
+        if constexpr (I8) qexp += 9;  // codes are held times 2^-9
+    }
+
+    auto tile_t0 = [&](int v) { return v < sp.ns ? kAttnTile * v : sp.start + kAttnTile * (v - sp.ns); };
+    // a token that is seen in the tile at t0
+    auto seen_in = [&](int t0) { return t0 < a.sinks ? t0 : max(t0, sp.ws); };
+    auto seen = [&](int t) { return t < sp.len && (t < a.sinks || t >= sp.ws); };
+    auto page_of = [&](int t) { return a.page_shift >= 0 ? t >> a.page_shift : t / a.page_size; };
+
+    uint32_t bad = 0;  // a page id outside the pool was met: the outputs are NaN
+
+    // Where the tile's rows are.  TILED: the page ids of the two sub-tiles and
+    // the slots that they begin at (a sub-tile with no token that is seen
+    // takes the other's place: its page may be gone).  Both are known one
+    // tile before its loads are issued.
+    struct At { int page[2], slot[2]; };
+    auto locate = [&](int v) __attribute__((always_inline)) {
+        At at;
+        const int t0 = tile_t0(v);
+        const int ts = seen_in(t0) & ~15;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            int t = t0 + 16 * u;
+            if (!(t < sp.len && (t < a.sinks || t + 16 > sp.ws))) t = ts;
+            const int p = page_of(t);
+            at.slot[u] = t - p * a.page_size;
+            at.page[u] = *(cint_t *)(uintptr_t)(a.table + seq * a.ld_table + p);
+        }
+        return at;
+    };
+    auto checked = [&](int page) __attribute__((always_inline)) {
+        const bool out = (unsigned)page >= (unsigned)a.n_pages;
+        bad |= out ? 1u : 0u;
+        return out ? 0 : page;
+    };
+
+    struct Kreg { u4_t w[2][KP]; float sc[2][4]; } kr;
+    struct Vreg { Bytes<VB> w[8]; float sc[8]; } vr;
+
+    // (sc of K: tokens 4g + i of the sub-tile, as the scores have them)
+    auto load_k_row = [&](const uint8_t *row, u4_t (&w)[KP]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int p = 0; p < KP; ++p) {
+            if constexpr (I8 && STEPS % 2 == 1) {
+                if (p == KP - 1) {
+                    u2_t h;
+                    __builtin_memcpy(&h, row + 64 * p + 8 * g, 8);
+                    w[p] = u4_t{h[0], h[1], 0, 0};
+                    continue;
+                }
+            }
+            __builtin_memcpy(&w[p], row + 64 * p + 16 * g, 16);
+        }
+    };
+    // the four rows of lane group g in sub-tile u, for the lane's own lookups
+    auto own_row = [&](int v, int t, int64_t &row, int64_t &sc) __attribute__((always_inline)) {
+        const int t0 = tile_t0(v);
+        if (!seen(t)) t = seen_in(t0);
+        const int p = page_of(t);
+        const int page = checked(a.table[seq * a.ld_table + p]);
+        const int slot = t - p * a.page_size;
+        row = page * a.page_stride + kvh * a.head_stride + slot * a.slot_stride;
+        sc = page * a.sc_page + kvh * a.sc_head + slot * a.sc_slot;
+    };
+    auto load_k = [&](int v, const At &at) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if constexpr (TILED) {
+                const int page = checked(at.page[u]);
+                const uint8_t *base = a.k + page * a.page_stride + kvh * a.head_stride + at.slot[u] * a.slot_stride;
+                load_k_row(base + (uint32_t)(j * (int)a.slot_stride), kr.w[u]);
+                if constexpr (I8) {
+                    const float *sb = a.ks + page * a.sc_page + kvh * a.sc_head + at.slot[u];
+                    __builtin_memcpy(kr.sc[u], sb + 4 * g, 16);
+                }
+            } else {
+                int64_t row, sc;
+                own_row(v, tile_t0(v) + 16 * u + j, row, sc);
+                load_k_row(a.k + row, kr.w[u]);
+                if constexpr (I8) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        own_row(v, tile_t0(v) + 16 * u + 4 * g + i, row, sc);
+                        kr.sc[u][i] = a.ks[sc];
+                    }
+                }
+            }
+        }
+    };
+    auto load_v = [&](int v, const At &at) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if constexpr (TILED) {
+                const int page = checked(at.page[u]);
+                const uint8_t *base = a.v + page * a.page_stride + kvh * a.head_stride + at.slot[u] * a.slot_stride;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    vr.w[4 * u + i] = load_bytes<VB>(base + (uint32_t)((4 * g + i) * (int)a.slot_stride + j * VB));
+                if constexpr (I8) {
+                    const float *sb = a.vs + page * a.sc_page + kvh * a.sc_head + at.slot[u];
+                    __builtin_memcpy(&vr.sc[4 * u], sb + 4 * g, 16);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    int64_t row, sc;
+                    own_row(v, tile_t0(v) + 16 * u + 4 * g + i, row, sc);
+                    vr.w[4 * u + i] = load_bytes<VB>(a.v + row + j * VB);
+                    if constexpr (I8) vr.sc[4 * u + i] = a.vs[sc];
+                }
+            }
+        }
+    };
+
+    f4_t o[DPL];
+#pragma unroll
+    for (int c = 0; c < DPL; ++c) o[c] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    float m = kAttnLow, l = 0.0f;
+    float vtop = 0.0f, vinv = 0.0f;  // power of two at or above the value scales met (8 bits), its inverse
+
+    float s[8];  // scores of tokens 4g + i (0..3) and 16 + 4g + i (4..7), in log2
+    auto scores = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            f4_t c = {0.0f, 0.0f, 0.0f, 0.0f}, d = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int st = 0; st < STEPS; ++st) {
+                h8_t kk;
+                if constexpr (I8) {
+                    const u4_t &w = kr.w[u][st >> 1];
+                    kk = codes8_f16(w[2 * (st & 1)], w[2 * (st & 1) + 1]);
+                } else {
+                    kk = __builtin_bit_cast(h8_t, kr.w[u][st]);
+                }
+                c = __builtin_amdgcn_mfma_f32_16x16x32_f16(kk, qh[st], c, 0, 0, 0);
+                d = __builtin_amdgcn_mfma_f32_16x16x32_f16(kk, ql[st], d, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float x = ldexpf(c[i] + d[i], qexp);
+                if constexpr (I8) x *= kr.sc[u][i];
+                s[4 * u + i] = x;
+            }
+        }
+    };
+    h8_t ph, pl;
+    // p from s, in place of what s was; the value scales go into ph and pl
+    auto probabilities = [&](int v) __attribute__((always_inline)) {
+        const int t0 = tile_t0(v);
+        const bool whole = t0 + kAttnTile <= sp.len && (t0 >= sp.ws || t0 + kAttnTile <= a.sinks);
+        uint32_t mask = 0xffu;
+        if (!whole) {
+            mask = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (seen(t0 + 16 * (i >> 2) + 4 * g + (i & 3))) mask |= 1u << i;
+                else s[i] = kAttnLow;
+        }
+        float top = s[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) top = fmaxf(top, s[i]);
+        top = quad_rows_max(top);
+        float vt = 0.0f;
+        if constexpr (I8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (!whole) vr.sc[i] = mask >> i & 1 ? vr.sc[i] : 0.0f;
+                vt = fmaxf(vt, fabsf(vr.sc[i]));
+            }
+            vt = quad_rows_max(vt);
+        }
+        if (__any(top > m || (I8 && vt > vtop))) {
+            const float mn = fmaxf(m, top);
+            float f = __builtin_amdgcn_exp2f(m - mn);
+            l *= f;
+            m = mn;
+            if constexpr (I8) {
+                if (vt > vtop) {
+                    int ex;
+                    (void)frexpf(vt, &ex);
+                    const float vn = ldexpf(1.0f, min(ex, 127));
+                    vinv = 1.0f / vn;
+                    f *= vtop * vinv;
+                    vtop = vn;
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < DPL; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[c][i] *= f;
+        }
+        const float mp = m - kAttnPexp;
+        float p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            p[i] = __builtin_amdgcn_exp2f(s[i] - mp);
+            if (!whole) p[i] = mask >> i & 1 ? p[i] : 0.0f;
+            l += p[i];
+        }
+        if constexpr (I8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] *= vr.sc[i] * vinv;
+        }
+        split8(p, ph, pl);
+        // rows that are not seen may hold anything, NaN included
+        if (!whole) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int d = 0; d < (VB + 3) / 4; ++d) vr.w[i].w[d] = mask >> i & 1 ? vr.w[i].w[d] : 0u;
+        }
+    };
+    auto outputs = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int c = 0; c < DPL; ++c) {
+            u4_t x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (I8) {
+                    const uint32_t e0 = vr.w[2 * i].w[c / 4], e1 = vr.w[2 * i + 1].w[c / 4];
+                    // byte c % 4 of both, moved from code to code + 128
+                    const uint32_t sel = 0x0c000c00u | (uint32_t)(c % 4) | ((uint32_t)(c % 4 + 4) << 16);
+                    x[i] = codes_f16(__builtin_amdgcn_perm(e1, e0, sel) ^ 0x00800080u);
+                } else {
+                    const uint32_t e0 = vr.w[2 * i].w[c / 2], e1 = vr.w[2 * i + 1].w[c / 2];
+                    x[i] = __builtin_amdgcn_perm(e1, e0, c % 2 ? 0x07060302u : 0x05040100u);
+                }
+            }
+            const h8_t vv = __builtin_bit_cast(h8_t, x);
+            o[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, ph, o[c], 0, 0, 0);
+            o[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, pl, o[c], 0, 0, 0);
+        }
+    };
+
+    // One register set: a tile's K registers are loaded again as soon as its
+    // scores are done, its V registers as soon as its outputs are.
+    int v = tbeg + wave;
+    if (v < tend) {
+        At at = locate(v);
+        load_k(v, at);
+        load_v(v, at);
+        at = locate(min(v + kAttnWaves, tend - 1));
+        for (; v + kAttnWaves < tend; v += kAttnWaves) {
+            const int n = v + kAttnWaves;
+            scores();
+            load_k(n, at);
+            probabilities(v);
+            outputs();
+            load_v(n, at);
+            at = locate(min(n + kAttnWaves, tend - 1));
+        }
+        scores();
+        probabilities(v);
+        outputs();
+    }
+    l = quad_rows_sum(l);
+    if (__any(bad)) l = __builtin_nanf("");
+
+    // join the waves
+    const float unit = I8 ? vtop * kCodeUnit : 1.0f;
+    if (g == 0) {
+        sm[wave][j][0] = m;
+        sm[wave][j][1] = l;
+    }
+    if (j < nh) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < DPL; ++c) so[wave][j][(4 * g + i) * DPL + c] = o[c][i] * unit;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < nh * (D / 4); i += 64 * kAttnWaves) {
+        const int h = i / (D / 4), d = 4 * (i % (D / 4));
+        float mm = sm[0][h][0];
+#pragma unroll
+        for (int w = 1; w < kAttnWaves; ++w) mm = fmaxf(mm, sm[w][h][0]);
+        f4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        float ll = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kAttnWaves; ++w) {
+            const float f = __builtin_amdgcn_exp2f(sm[w][h][0] - mm);
+            ll += f * sm[w][h][1];
+            const f4_t x = *reinterpret_cast<const f4_t *>(&so[w][h][d]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] += f * x[e];
+        }
+        const int head = head0 + h;
+        if (sp.tiles <= a.chunk_tiles) {
+            // the only chunk
+            const int64_t at = seq * a.y_seq + head * a.y_head + d;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float y = acc[e] / ll;
+                if (a.out_f16) static_cast<uint16_t *>(a.y)[at + e] = f2h(y);
+                else static_cast<float *>(a.y)[at + e] = y;
+            }
+        } else {
+            float *part = a.part + ((int64_t)(seq * (int64_t)a.n_heads + head) * a.nchunks + chunk) * attn_part_floats(D);
+            if (d == 0) {
+                part[0] = mm;
+                part[1] = ll;
+            }
+            *reinterpret_cast<f4_t *>(part + 4 + d) = acc;
+        }
+    }
+}
+
+// Joins the chunks of one (sequence, head): a workgroup's threads take the
+// partial results D/4 threads at a time.
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
+    constexpr int COLS = D / 4;
+    constexpr int ROWS = 256 / COLS;   // chunks at a time
+    __shared__ __attribute__((aligned(16))) float so[ROWS][D];
+    __shared__ float sl[ROWS];
+    const int head = blockIdx.x % a.n_heads;
+    const int seq = blockIdx.x / a.n_heads;
+    const int len_in = a.lens[seq];
+    const AttnSpan sp = attn_span(len_in < 0 || len_in > a.max_len ? 0 : len_in, a.window, a.sinks);
+    const int n = (sp.tiles + a.chunk_tiles - 1) / a.chunk_tiles;
+    if (n <= 1) return;  // written already (whole workgroup, before any barrier)
+    const float *part = a.part + (int64_t)(seq * (int64_t)a.n_heads + head) * a.nchunks * attn_part_floats(D);
+    float m = kAttnLow;
+    for (int c = threadIdx.x & 63; c < n; c += 64) m = fmaxf(m, part[c * attn_part_floats(D)]);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+    const int row = threadIdx.x / COLS, col = threadIdx.x % COLS;
+    if (row < ROWS) {
+        f4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        float l = 0.0f;
+        for (int c = row; c < n; c += ROWS) {
+            const float *p = part + c * attn_part_floats(D);
+            const float f = __builtin_amdgcn_exp2f(p[0] - m);
+            l += f * p[1];
+            const f4_t x = *reinterpret_cast<const f4_t *>(p + 4 + 4 * col);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] += f * x[e];
+        }
+        *reinterpret_cast<f4_t *>(&so[row][4 * col]) = acc;
+        if (col == 0) sl[row] = l;
+    }
+    __syncthreads();
+    for (int d = threadIdx.x; d < D; d += 256) {
+        float acc = 0.0f, l = 0.0f;
+        for (int r = 0; r < ROWS; ++r) {
+            acc += so[r][d];
+            l += sl[r];
+        }
+        const float y = acc / l;
+        const int64_t at = seq * a.y_seq + head * a.y_head + d;
+        if (a.out_f16) static_cast<uint16_t *>(a.y)[at] = f2h(y);
+        else static_cast<float *>(a.y)[at] = y;
+    }
+}
+
+template <int D, bool I8>
+int attn_decode_dim(const AttnArgs &a, bool tiled, hipStream_t stream) {
+    const dim3 grid((unsigned)((int64_t)a.n_seqs * a.n_kv * a.head_tiles * a.nchunks));
+    const int st = tiled ? launch(attn_decode_kernel<D, I8, true>, grid, dim3(64 * kAttnWaves), stream, a)
+                         : launch(attn_decode_kernel<D, I8, false>, grid, dim3(64 * kAttnWaves), stream, a);
+    if (st != QK_OK || a.nchunks == 1) return st;
+    return launch(attn_join_kernel<D>, dim3((unsigned)(a.n_seqs * (int64_t)a.n_heads)), dim3(256), stream, a);
+}
+
+template <bool I8>
+int attn_decode_run(const AttnArgs &a, int head_dim, bool tiled, hipStream_t stream) {
+    switch (head_dim) {
+    case 32: return attn_decode_dim<32, I8>(a, tiled, stream);
+    case 64: return attn_decode_dim<64, I8>(a, tiled, stream);
+    case 96: return attn_decode_dim<96, I8>(a, tiled, stream);
+    case 128: return attn_decode_dim<128, I8>(a, tiled, stream);
+    case 160: return attn_decode_dim<160, I8>(a, tiled, stream);
+    case 192: return attn_decode_dim<192, I8>(a, tiled, stream);
+    case 224: return attn_decode_dim<224, I8>(a, tiled, stream);
+    case 256: return attn_decode_dim<256, I8>(a, tiled, stream);
+    default: return QK_ERR_INVALID_ARG;
+    }
+}
+
+}  // namespace qk

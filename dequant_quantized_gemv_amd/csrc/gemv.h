@@ -60,8 +60,14 @@ struct GemvExpert {
 template <int NC>
 int gemv_table(int fmt, GemvArgs &a, bool fast, hipStream_t stream);
 
+// Where 8-bit activations come from: quantized while they are staged, or
+// blocks of kX8BlockBytes (fp32 scale, 32 codes) that the caller has; then
+// GemvItem::x is the blocks' address and ldx the dwords between columns.
+enum GemvX8 { kX8None = 0, kX8Quantize = 1, kX8Stored = 2 };
+constexpr int kX8BlockBytes = 36;
+
 // The same with 8-bit activations (integer dot products); one problem only.
-template <int NC>
+template <int NC, int X8>
 int gemv_table_x8(int fmt, GemvArgs &a, bool fast, hipStream_t stream);
 
 // Launch expert-indexed problems (same `fast` condition, for every expert and

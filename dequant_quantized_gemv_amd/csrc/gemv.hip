@@ -94,8 +94,10 @@ int launch_mul_mat_vec_batched(int fmt, const qk_mat_vec_item *items, int count,
     return gemv_by_columns(fmt, a, (int)n, fast, stream);
 }
 
-int launch_mul_mat_vec_x8(int fmt, const void *w, int64_t m, int64_t k, const float *x,
-                          int64_t n, int64_t ldx, float *y, int64_t ldy, hipStream_t stream) {
+// One problem with 8-bit activations; x and ldx as GemvItem takes them for X8.
+template <int X8>
+static int launch_x8(int fmt, const void *w, int64_t m, int64_t k, const float *x, int64_t n, int64_t ldx,
+                     float *y, int64_t ldy, hipStream_t stream) {
     if (k == 0) {
         // no weights: every output is the empty sum
         GemvExpert z{};
@@ -118,16 +120,26 @@ int launch_mul_mat_vec_x8(int fmt, const void *w, int64_t m, int64_t k, const fl
     a.count = 1;
     const bool fast = ((uintptr_t)d.w % 4) == 0 && (d.nb % 2) == 0;
     switch (n) {
-    case 1: return gemv_table_x8<1>(fmt, a, fast, stream);
-    case 2: return gemv_table_x8<2>(fmt, a, fast, stream);
-    case 3: return gemv_table_x8<3>(fmt, a, fast, stream);
-    case 4: return gemv_table_x8<4>(fmt, a, fast, stream);
-    case 5: return gemv_table_x8<5>(fmt, a, fast, stream);
-    case 6: return gemv_table_x8<6>(fmt, a, fast, stream);
-    case 7: return gemv_table_x8<7>(fmt, a, fast, stream);
-    case 8: return gemv_table_x8<8>(fmt, a, fast, stream);
+    case 1: return gemv_table_x8<1, X8>(fmt, a, fast, stream);
+    case 2: return gemv_table_x8<2, X8>(fmt, a, fast, stream);
+    case 3: return gemv_table_x8<3, X8>(fmt, a, fast, stream);
+    case 4: return gemv_table_x8<4, X8>(fmt, a, fast, stream);
+    case 5: return gemv_table_x8<5, X8>(fmt, a, fast, stream);
+    case 6: return gemv_table_x8<6, X8>(fmt, a, fast, stream);
+    case 7: return gemv_table_x8<7, X8>(fmt, a, fast, stream);
+    case 8: return gemv_table_x8<8, X8>(fmt, a, fast, stream);
     default: return QK_ERR_INVALID_ARG;
     }
+}
+
+int launch_mul_mat_vec_x8(int fmt, const void *w, int64_t m, int64_t k, const float *x,
+                          int64_t n, int64_t ldx, float *y, int64_t ldy, hipStream_t stream) {
+    return launch_x8<kX8Quantize>(fmt, w, m, k, x, n, ldx, y, ldy, stream);
+}
+
+int launch_mul_mat_vec_x8q(int fmt, const void *w, int64_t m, int64_t k, const void *xq,
+                           int64_t n, int64_t ldx, float *y, int64_t ldy, hipStream_t stream) {
+    return launch_x8<kX8Stored>(fmt, w, m, k, static_cast<const float *>(xq), n, ldx / 4, y, ldy, stream);
 }
 
 int launch_mul_mat_vec(int fmt, const void *w, int64_t m, int64_t k, const float *x,

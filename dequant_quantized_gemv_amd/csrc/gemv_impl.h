@@ -491,6 +491,17 @@ __device__ __forceinline__ void x8_block(const f32x4_t (&v)[8], uint8_t *codes, 
     *reinterpret_cast<u32x2_t *>(scale) = u32x2_t{__builtin_bit_cast(uint32_t, d), (uint32_t)qsum};
 }
 
+// A stored block (scale, then 32 codes) to the same place, with the sum of
+// its codes.
+__device__ __forceinline__ void x8_copy(const uint32_t (&v)[9], uint8_t *codes, uint8_t *scale) {
+    int qsum = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) qsum = __builtin_amdgcn_sdot4((int)v[1 + i], 0x01010101, qsum, false);
+    *reinterpret_cast<u32x4_t *>(codes) = u32x4_t{v[1], v[2], v[3], v[4]};
+    *reinterpret_cast<u32x4_t *>(codes + 16) = u32x4_t{v[5], v[6], v[7], v[8]};
+    *reinterpret_cast<u32x2_t *>(scale) = u32x2_t{v[0], (uint32_t)qsum};
+}
+
 // Integer-dot products of one wave's RWV rows with this lane's pair (pair pw
 // of the window) against 8-bit activations, added to acc: per block and
 // column, eight 4-way int8 dot products (exact), then one scaled add,
@@ -604,7 +615,7 @@ __host__ __device__ constexpr int seg_store_lane(int lpr) { return lpr == 32 ? 3
 // offsets and no indexed reads of a table before the first weight load;
 // kSrcExpert reads each problem's expert id from device memory when a step
 // enters the problem (an id outside the stack reads expert 0 and stores NaN).
-template <int FMT, int NC, int RWV, int WPG, bool FAST, int SRC, int SUB, bool X8>
+template <int FMT, int NC, int RWV, int WPG, bool FAST, int SRC, int SUB, int X8>
 __global__ __launch_bounds__(64 * WPG) __attribute__((amdgpu_waves_per_eu(NC == 1 || (NC == 2 && FMT != QK_Q8_0) ? 4 : (NC == 2 ? 2 : 1)))) void gemv_kernel(const typename GemvSrc<SRC>::Args args, const GemvSplit split) {
     static_assert(SUB == 0 || RWV == 1, "several rows per wave only with one row per segment");
     static_assert(SRC != kSrcExpert || NC == 1, "expert-indexed problems have one column");
@@ -814,28 +825,38 @@ __global__ __launch_bounds__(64 * WPG) __attribute__((amdgpu_waves_per_eu(NC == 
 
     // 8-bit activations: block bi of the window (columns one after another,
     // nblk blocks each) is read from x and quantized into LDS.
+    // Stored blocks (it.x their address, it.ldx the dwords between columns)
+    // are copied, which makes the same bytes in LDS.
     auto x8_src = [&](const GemvItem &it, int e0, int nblk, int bi) -> const float * {
         const int j = bi / nblk;
+        if constexpr (X8 == kX8Stored) return it.x + j * it.ldx + (e0 / 32 + bi - j * nblk) * (kX8BlockBytes / 4);
         return it.x + j * it.ldx + e0 + 32 * (bi - j * nblk);
     };
-    auto x8_load = [&](const float *src, f32x4_t (&v)[8]) __attribute__((always_inline)) {
+    using X8Regs = std::conditional_t<X8 == kX8Stored, uint32_t[9], f32x4_t[8]>;
+    auto x8_load = [&](const float *src, X8Regs &v) __attribute__((always_inline)) {
+        if constexpr (X8 == kX8Stored) {
+            __builtin_memcpy(v, src, kX8BlockBytes);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const f32x4_a4 *>(src + 4 * i);
+            for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const f32x4_a4 *>(src + 4 * i);
+        }
     };
-    auto x8_put = [&](int nblk, int bi, const f32x4_t (&v)[8]) __attribute__((always_inline)) {
+    auto x8_put = [&](int nblk, int bi, const X8Regs &v) __attribute__((always_inline)) {
         const int j = bi / nblk;
         const int bb = bi - j * nblk;
         uint8_t *col = xq + j * kX8ColBytes;
-        x8_block(v, col + kX8PairPitch * (bb >> 1) + 32 * (bb & 1), col + kX8ScaleOff + 8 * bb);
+        uint8_t *codes = col + kX8PairPitch * (bb >> 1) + 32 * (bb & 1), *scale = col + kX8ScaleOff + 8 * bb;
+        if constexpr (X8 == kX8Stored) x8_copy(v, codes, scale);
+        else x8_block(v, codes, scale);
     };
 
     // Copy window `wi` of problem `it`'s activations into LDS (whole workgroup).
     auto stage_x = [&](const GemvItem &it, int wi) __attribute__((always_inline)) {
         const int e0 = wi * XW;
-        if constexpr (X8) {
+        if constexpr (X8 != kX8None) {
             const int nblk = min(XW, it.nb * 32 - e0) / 32;
             for (int bi = tid; bi < NC * nblk; bi += NT) {
-                f32x4_t v[8];
+                X8Regs v;
                 x8_load(x8_src(it, e0, nblk, bi), v);
                 x8_put(nblk, bi, v);
             }
@@ -920,7 +941,7 @@ __global__ __launch_bounds__(64 * WPG) __attribute__((amdgpu_waves_per_eu(NC == 
         const Pos Q = advance(P);
         const Pos PF = Q.g < gend ? Q : P;
 
-        if constexpr (FIRST && X8) {
+        if constexpr (FIRST && X8 != kX8None) {
             // one block of activations per thread loaded first, then the
             // weights, then quantization into LDS (waits only for the
             // activations); a tail thread repeats the last block
@@ -928,7 +949,7 @@ __global__ __launch_bounds__(64 * WPG) __attribute__((amdgpu_waves_per_eu(NC == 
             const int nblk = min(XW, it.nb * 32 - e0) / 32;
             const int tb = NC * nblk;
             const int b0 = min(tid, tb - 1);
-            f32x4_t xr8[8];
+            X8Regs xr8;
             x8_load(x8_src(it, e0, nblk, b0), xr8);
             // (the empty asm statements keep the three groups of loads in
             // this order and ahead of the quantization, which then waits for
@@ -942,7 +963,7 @@ __global__ __launch_bounds__(64 * WPG) __attribute__((amdgpu_waves_per_eu(NC == 
             asm volatile("" ::: "memory");
             x8_put(nblk, b0, xr8);
             for (int bi = tid + NT; bi < tb; bi += NT) {
-                f32x4_t v[8];
+                X8Regs v;
                 x8_load(x8_src(it, e0, nblk, bi), v);
                 x8_put(nblk, bi, v);
             }
@@ -1013,7 +1034,7 @@ __global__ __launch_bounds__(64 * WPG) __attribute__((amdgpu_waves_per_eu(NC == 
         const int pp = P.c * G.lpr + G.sl;
         if (nrows > 0 && pp < npairs) {
             const int el = (P.c - (wi << swl)) * (64 * G.lpr) + G.sl * 64;  // window element of the pair
-            if constexpr (X8)
+            if constexpr (X8 != kX8None)
                 pair_dot_x8<FMT, NC, RWV, FAST>(cur, nrows, FAST || (2 * pp + 1 < it.nb), xq, el >> 6, acc);
             else
                 pair_dot<FMT, NC, RWV, FAST>(cur, nrows, FAST || (2 * pp + 1 < it.nb), xs, XP, el, acc);
@@ -1099,7 +1120,7 @@ __global__ __launch_bounds__(64 * WPG) __attribute__((amdgpu_waves_per_eu(NC == 
 // spills with two rows per wave) above 32 rows per CU: Q4_1 11008 x 4096
 // 11.4 -> 10.6 us at 2 columns, 15.6 -> 14.0 us at 3; at 4096 rows it loses
 // (5.5 -> 6.3 and 7.1 -> 7.6 us).
-template <int FMT, int NC, int SUB, bool FAST, bool X8 = false, bool R2 = false> struct GemvShape {
+template <int FMT, int NC, int SUB, bool FAST, int X8 = kX8None, bool R2 = false> struct GemvShape {
     static_assert(!R2 || (NC <= 3 && SUB == 0 && !X8 && (NC == 1 || (FMT != QK_Q8_0 && (!kHasM<FMT> || FAST)))),
                   "two rows per wave: up to 3 columns, full-wave rows");
     static constexpr bool kWideQ41Generic = kHasM<FMT> && NC > 4 && !FAST;
@@ -1134,9 +1155,14 @@ constexpr int kGvMaxWgPerCu = QK_GEMV_WG_PER_CU;
 #define QK_GEMV_X8_WG_PER_CU 1
 #endif
 constexpr int kGvX8MaxWgPerCu = QK_GEMV_X8_WG_PER_CU;
+// Stored blocks cost a workgroup a copy and no quantization.
+#ifndef QK_GEMV_X8Q_WG_PER_CU
+#define QK_GEMV_X8Q_WG_PER_CU 4
+#endif
+constexpr int kGvX8StoredMaxWgPerCu = QK_GEMV_X8Q_WG_PER_CU;
 
 // One launch over `total` row groups (gpi per problem for expert launches).
-template <int FMT, int NC, int SRC, int SUB, bool FAST, bool X8, bool R2 = false>
+template <int FMT, int NC, int SRC, int SUB, bool FAST, int X8, bool R2 = false>
 int gemv_launch(const typename GemvSrc<SRC>::Args &args, int64_t total, int gpi, hipStream_t stream) {
     constexpr int RWV = GemvShape<FMT, NC, SUB, FAST, X8, R2>::kRWV;
     constexpr int WPG = GemvShape<FMT, NC, SUB, FAST, X8, R2>::kWPG;
@@ -1148,7 +1174,8 @@ int gemv_launch(const typename GemvSrc<SRC>::Args &args, int64_t total, int gpi,
     // 11008 weights.
     // (8-bit activations: 6 KiB per column)
     const size_t lds = X8 ? (size_t)NC * kX8ColBytes : (size_t)NC * kGvPitch * sizeof(float);
-    const int per_cu = max(1, min(X8 ? kGvX8MaxWgPerCu : kGvMaxWgPerCu, (int)((160 * 1024) / lds)));
+    constexpr int kMaxPerCu = X8 == kX8Stored ? kGvX8StoredMaxWgPerCu : X8 == kX8Quantize ? kGvX8MaxWgPerCu : kGvMaxWgPerCu;
+    const int per_cu = max(1, min(kMaxPerCu, (int)((160 * 1024) / lds)));
     const int64_t cap = (int64_t)device_cus() * per_cu;
     const int nwg = (int)(total < cap ? total : cap);
     const GemvSplit split{(int)total, (int)total / nwg, (int)total % nwg, gpi};
@@ -1160,7 +1187,7 @@ int gemv_launch(const typename GemvSrc<SRC>::Args &args, int64_t total, int gpi,
     return launch_lds(kern, dim3((unsigned)nwg), dim3(64 * WPG), lds, stream, args, split);
 }
 
-template <int FMT, int NC, int SUB, bool FAST, bool X8, bool R2 = false>
+template <int FMT, int NC, int SUB, bool FAST, int X8, bool R2 = false>
 int gemv_table_run(GemvArgs &a, hipStream_t stream) {
     constexpr int RG = GemvShape<FMT, NC, SUB, FAST, X8, R2>::kRowsPerGroup;
     int64_t g = 0;
@@ -1172,15 +1199,15 @@ int gemv_table_run(GemvArgs &a, hipStream_t stream) {
         a.gbase[i + 1] = (int)g;
     }
     if constexpr (SUB == kSubMixed) {
-        return gemv_launch<FMT, NC, kSrcTable, SUB, FAST, false, false>(a, g, 0, stream);  // count > 1
+        return gemv_launch<FMT, NC, kSrcTable, SUB, FAST, kX8None, false>(a, g, 0, stream);  // count > 1
     } else {
         if (a.count == 1) return gemv_launch<FMT, NC, kSrcOne, SUB, FAST, X8, R2>(a.item[0], g, 0, stream);
-        if constexpr (X8) return QK_ERR_INVALID_ARG;  // 8-bit activations: one problem per launch
-        else return gemv_launch<FMT, NC, kSrcTable, SUB, FAST, false, R2>(a, g, 0, stream);
+        if constexpr (X8 != kX8None) return QK_ERR_INVALID_ARG;  // 8-bit activations: one problem per launch
+        else return gemv_launch<FMT, NC, kSrcTable, SUB, FAST, kX8None, R2>(a, g, 0, stream);
     }
 }
 
-template <int FMT, int NC, int SUB, bool X8>
+template <int FMT, int NC, int SUB, int X8>
 int gemv_table_sub(GemvArgs &a, bool fast, hipStream_t stream) {
     if constexpr (NC <= 3 && SUB == 0 && !X8 && (NC == 1 || FMT != QK_Q8_0)) {
         int64_t rows = 0;
@@ -1201,7 +1228,7 @@ int gemv_table_sub(GemvArgs &a, bool fast, hipStream_t stream) {
 template <int FMT, int NC>
 int gemv_mfma_launch(const GemvItem &it, hipStream_t stream);
 
-template <int FMT, int NC, bool X8>
+template <int FMT, int NC, int X8>
 int gemv_table_fmt(GemvArgs &a, bool fast, hipStream_t stream) {
     if constexpr (NC >= 4 && !X8) {
         if (a.count == 1 && fast && a.item[0].nb * kBlockElems <= kGvWindow) {
@@ -1214,7 +1241,7 @@ int gemv_table_fmt(GemvArgs &a, bool fast, hipStream_t stream) {
             // matrix cores measured as fast or faster.
             bool vector_alu = false;
             if constexpr (NC == 4) {
-                constexpr int RG = GemvShape<FMT, NC, 0, true, false>::kRowsPerGroup;
+                constexpr int RG = GemvShape<FMT, NC, 0, true>::kRowsPerGroup;
                 const int64_t groups = ((int64_t)a.item[0].m + RG - 1) / RG;
                 const int slots =
                     max(1, min(kGvMaxWgPerCu, (int)((160 * 1024) / ((size_t)NC * kGvPitch * sizeof(float)))));
@@ -1236,8 +1263,8 @@ int gemv_table_fmt(GemvArgs &a, bool fast, hipStream_t stream) {
         // tensor-parallel share: 8-pair and 64-pair rows) keep their own
         if constexpr (!X8) {
             if (mixed && a.count > 1) {
-                if (fast) return gemv_table_run<FMT, NC, kSubMixed, true, false>(a, stream);
-                return gemv_table_run<FMT, NC, kSubMixed, false, false>(a, stream);
+                if (fast) return gemv_table_run<FMT, NC, kSubMixed, true, kX8None>(a, stream);
+                return gemv_table_run<FMT, NC, kSubMixed, false, kX8None>(a, stream);
             }
         }
         switch (gemv_sub(npairs)) {
@@ -1253,23 +1280,24 @@ int gemv_table_fmt(GemvArgs &a, bool fast, hipStream_t stream) {
 template <int NC>
 int gemv_table(int fmt, GemvArgs &a, bool fast, hipStream_t stream) {
     switch (fmt) {
-    case QK_Q4_0: return gemv_table_fmt<QK_Q4_0, NC, false>(a, fast, stream);
-    case QK_Q4_1: return gemv_table_fmt<QK_Q4_1, NC, false>(a, fast, stream);
-    case QK_Q8_0: return gemv_table_fmt<QK_Q8_0, NC, false>(a, fast, stream);
-    case QK_Q5_0: return gemv_table_fmt<QK_Q5_0, NC, false>(a, fast, stream);
-    case QK_Q5_1: return gemv_table_fmt<QK_Q5_1, NC, false>(a, fast, stream);
+    case QK_Q4_0: return gemv_table_fmt<QK_Q4_0, NC, kX8None>(a, fast, stream);
+    case QK_Q4_1: return gemv_table_fmt<QK_Q4_1, NC, kX8None>(a, fast, stream);
+    case QK_Q8_0: return gemv_table_fmt<QK_Q8_0, NC, kX8None>(a, fast, stream);
+    case QK_Q5_0: return gemv_table_fmt<QK_Q5_0, NC, kX8None>(a, fast, stream);
+    case QK_Q5_1: return gemv_table_fmt<QK_Q5_1, NC, kX8None>(a, fast, stream);
     default: return QK_ERR_INVALID_ARG;
     }
 }
 
-template <int NC>
+template <int NC, int X8>
 int gemv_table_x8(int fmt, GemvArgs &a, bool fast, hipStream_t stream) {
+    static_assert(X8 != kX8None, "8-bit activations");
     switch (fmt) {
-    case QK_Q4_0: return gemv_table_fmt<QK_Q4_0, NC, true>(a, fast, stream);
-    case QK_Q4_1: return gemv_table_fmt<QK_Q4_1, NC, true>(a, fast, stream);
-    case QK_Q8_0: return gemv_table_fmt<QK_Q8_0, NC, true>(a, fast, stream);
-    case QK_Q5_0: return gemv_table_fmt<QK_Q5_0, NC, true>(a, fast, stream);
-    case QK_Q5_1: return gemv_table_fmt<QK_Q5_1, NC, true>(a, fast, stream);
+    case QK_Q4_0: return gemv_table_fmt<QK_Q4_0, NC, X8>(a, fast, stream);
+    case QK_Q4_1: return gemv_table_fmt<QK_Q4_1, NC, X8>(a, fast, stream);
+    case QK_Q8_0: return gemv_table_fmt<QK_Q8_0, NC, X8>(a, fast, stream);
+    case QK_Q5_0: return gemv_table_fmt<QK_Q5_0, NC, X8>(a, fast, stream);
+    case QK_Q5_1: return gemv_table_fmt<QK_Q5_1, NC, X8>(a, fast, stream);
     default: return QK_ERR_INVALID_ARG;
     }
 }
@@ -1278,7 +1306,7 @@ template <int FMT, int SUB, bool FAST>
 int gemv_expert_run(const GemvExpert &e, hipStream_t stream) {
     constexpr int RG = GemvShape<FMT, 1, SUB, FAST>::kRowsPerGroup;
     const int gpi = (e.m + RG - 1) / RG;
-    return gemv_launch<FMT, 1, kSrcExpert, SUB, FAST, false>(e, (int64_t)gpi * e.count, gpi, stream);
+    return gemv_launch<FMT, 1, kSrcExpert, SUB, FAST, kX8None>(e, (int64_t)gpi * e.count, gpi, stream);
 }
 
 template <int FMT, int SUB>

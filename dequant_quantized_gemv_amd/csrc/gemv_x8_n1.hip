@@ -4,6 +4,6 @@
 
 namespace qk {
 
-template int gemv_table_x8<1>(int fmt, GemvArgs &a, bool fast, hipStream_t stream);
+template int gemv_table_x8<1, kX8Quantize>(int fmt, GemvArgs &a, bool fast, hipStream_t stream);
 
 }  // namespace qk

@@ -4,8 +4,8 @@
 
 namespace qk {
 
-template int gemv_table_x8<2>(int fmt, GemvArgs &a, bool fast, hipStream_t stream);
-template int gemv_table_x8<3>(int fmt, GemvArgs &a, bool fast, hipStream_t stream);
-template int gemv_table_x8<4>(int fmt, GemvArgs &a, bool fast, hipStream_t stream);
+template int gemv_table_x8<2, kX8Quantize>(int fmt, GemvArgs &a, bool fast, hipStream_t stream);
+template int gemv_table_x8<3, kX8Quantize>(int fmt, GemvArgs &a, bool fast, hipStream_t stream);
+template int gemv_table_x8<4, kX8Quantize>(int fmt, GemvArgs &a, bool fast, hipStream_t stream);
 
 }  // namespace qk

@@ -4,9 +4,9 @@
 
 namespace qk {
 
-template int gemv_table_x8<5>(int fmt, GemvArgs &a, bool fast, hipStream_t stream);
-template int gemv_table_x8<6>(int fmt, GemvArgs &a, bool fast, hipStream_t stream);
-template int gemv_table_x8<7>(int fmt, GemvArgs &a, bool fast, hipStream_t stream);
-template int gemv_table_x8<8>(int fmt, GemvArgs &a, bool fast, hipStream_t stream);
+template int gemv_table_x8<5, kX8Quantize>(int fmt, GemvArgs &a, bool fast, hipStream_t stream);
+template int gemv_table_x8<6, kX8Quantize>(int fmt, GemvArgs &a, bool fast, hipStream_t stream);
+template int gemv_table_x8<7, kX8Quantize>(int fmt, GemvArgs &a, bool fast, hipStream_t stream);
+template int gemv_table_x8<8, kX8Quantize>(int fmt, GemvArgs &a, bool fast, hipStream_t stream);
 
 }  // namespace qk

@@ -57,6 +57,10 @@ int launch_mul_mat_vec(int fmt, const void *w, int64_t m, int64_t k, const float
 int launch_mul_mat_vec_x8(int fmt, const void *w, int64_t m, int64_t k, const float *x,
                           int64_t n, int64_t ldx, float *y, int64_t ldy, hipStream_t stream);
 
+// ldx: bytes between columns of 8-bit activation blocks
+int launch_mul_mat_vec_x8q(int fmt, const void *w, int64_t m, int64_t k, const void *xq,
+                           int64_t n, int64_t ldx, float *y, int64_t ldy, hipStream_t stream);
+
 int launch_mul_mat_vec_batched(int fmt, const qk_mat_vec_item *items, int count, int64_t n,
                                hipStream_t stream);
 
@@ -68,5 +72,17 @@ int launch_mul_mat_vec_id(int fmt, const void *w, int64_t n_experts, int64_t exp
 
 int launch_mul_mat(int fmt, const void *w, int64_t m, int64_t k, const uint16_t *x,
                    int64_t n, int64_t ldx, float *y, int64_t ldy, hipStream_t stream);
+
+// lds: of sum; ldy in bytes for QK_X8 outputs
+int launch_rms_norm(int x_dtype, const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                    const float *weight, double eps, int64_t n, int64_t k, void *sum, int64_t lds,
+                    int y_dtype, void *y, int64_t ldy, hipStream_t stream);
+
+struct StoreArgs;  // attn.h
+int launch_kv_store(const StoreArgs &a, bool i8, hipStream_t stream);
+
+int launch_moe_route(const float *x, int64_t ldx, int64_t n, int64_t experts, int64_t used, bool sigmoid,
+                     const float *bias, int64_t groups, int64_t kept, int64_t best, bool renorm, float scale,
+                     int32_t *ids, int64_t ld_ids, float *w, int64_t ldw, hipStream_t stream);
 
 }  // namespace qk

@@ -14,14 +14,18 @@ LIB_PATH = os.path.join(PKG, "libqk.so")
 
 # enum qk_format / qk_dtype / qk_status (include/qk.h)
 QK_Q4_0, QK_Q4_1, QK_Q8_0, QK_Q5_0, QK_Q5_1 = 1, 2, 3, 4, 5
-QK_F32, QK_F16 = 0, 1
+QK_F32, QK_F16, QK_X8 = 0, 1, 2
+QK_KV_F16, QK_KV_I8 = 0, 1
+QK_SOFTMAX, QK_SIGMOID = 0, 1
 QK_OK, QK_ERR_INVALID_ARG, QK_ERR_UNSUPPORTED, QK_ERR_ALIGNMENT, QK_ERR_LAUNCH = 0, 1, 2, 3, 4
 
 FORMATS = {"q4_0": QK_Q4_0, "q4_1": QK_Q4_1, "q8_0": QK_Q8_0, "q5_0": QK_Q5_0, "q5_1": QK_Q5_1}
 SYMBOLS = ("qk_block_bytes", "qk_row_bytes", "qk_status_string", "qk_version",
            "qk_dequantize", "qk_mul_mat_vec", "qk_mul_mat_vec_x8", "qk_mul_mat_vec_batched",
-           "qk_mul_mat_vec_id", "qk_mul_mat")
+           "qk_mul_mat_vec_id", "qk_mul_mat", "qk_mul_mat_vec_x8q", "qk_rms_norm", "qk_kv_store",
+           "qk_attn_decode", "qk_attn_decode_workspace", "qk_moe_route")
 QK_MAX_BATCH = 16
+X8_BLOCK_BYTES = 36  # an 8-bit activation block: fp32 scale, 32 int8 codes
 
 
 class MatVecItem(ctypes.Structure):
@@ -29,6 +33,17 @@ class MatVecItem(ctypes.Structure):
     _fields_ = [("w", ctypes.c_void_p), ("m", ctypes.c_int64), ("k", ctypes.c_int64),
                 ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
                 ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64)]
+
+
+class KVCacheDesc(ctypes.Structure):
+    """struct qk_kv_cache (include/qk.h)."""
+    _fields_ = [("type", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int64), ("n_heads", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("head_dim", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
+                ("scale_page_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64),
+                ("scale_slot_stride", ctypes.c_int64)]
 
 
 class QKError(RuntimeError):
@@ -71,6 +86,21 @@ def load():
     lib.qk_mul_mat_vec_id.restype = ci
     lib.qk_mul_mat.argtypes = [ci, vp, i64, i64, vp, i64, i64, vp, i64, vp]
     lib.qk_mul_mat.restype = ci
+    lib.qk_mul_mat_vec_x8q.argtypes = [ci, vp, i64, i64, vp, i64, i64, vp, i64, vp]
+    lib.qk_mul_mat_vec_x8q.restype = ci
+    lib.qk_rms_norm.argtypes = [ci, vp, i64, vp, i64, vp, ctypes.c_double, i64, i64, vp, i64, ci, vp, i64, vp]
+    lib.qk_rms_norm.restype = ci
+    cache = ctypes.POINTER(KVCacheDesc)
+    lib.qk_kv_store.argtypes = [cache, vp, i64, i64, vp, i64, i64, i64, vp, i64, i64, i64, vp, vp, vp]
+    lib.qk_kv_store.restype = ci
+    lib.qk_attn_decode.argtypes = [cache, vp, i64, i64, i64, i64, vp, i64, vp, i64, ctypes.c_float, i64, i64,
+                                   ci, vp, i64, i64, vp, ctypes.c_size_t, vp]
+    lib.qk_attn_decode.restype = ci
+    lib.qk_attn_decode_workspace.argtypes = [cache, i64, i64, i64, i64, i64]
+    lib.qk_attn_decode_workspace.restype = ctypes.c_size_t
+    lib.qk_moe_route.argtypes = [vp, i64, i64, i64, i64, ci, vp, i64, i64, i64, ci, ctypes.c_float,
+                                 vp, i64, vp, i64, vp]
+    lib.qk_moe_route.restype = ci
     _lib = lib
     return lib
 
@@ -145,6 +175,41 @@ def qk_mul_mat_vec_id(fmt, w_ptr, n_experts, expert_stride, m, k, ids_ptr, ld_id
 
 def qk_mul_mat(fmt, w_ptr, m, k, x_ptr, n, ldx, y_ptr, ldy, stream=0):
     return load().qk_mul_mat(_fmt(fmt), w_ptr, m, k, x_ptr, n, ldx, y_ptr, ldy, stream)
+
+
+def qk_mul_mat_vec_x8q(fmt, w_ptr, m, k, xq_ptr, n, ldx, y_ptr, ldy, stream=0):
+    return load().qk_mul_mat_vec_x8q(_fmt(fmt), w_ptr, m, k, xq_ptr, n, ldx, y_ptr, ldy, stream)
+
+
+def qk_rms_norm(x_dtype, x_ptr, ldx, residual_ptr, ldr, weight_ptr, eps, n, k, sum_ptr, lds, y_dtype, y_ptr,
+                ldy, stream=0):
+    return load().qk_rms_norm(x_dtype, x_ptr, ldx, residual_ptr, ldr, weight_ptr, eps, n, k, sum_ptr, lds,
+                              y_dtype, y_ptr, ldy, stream)
+
+
+def qk_kv_store(cache, k_ptr, k_tok, k_head, v_ptr, v_tok, v_head, n_tokens, table_ptr, ld_table, n_seqs,
+                max_pages, seq_ptr, pos_ptr, stream=0):
+    """cache: a KVCacheDesc or None."""
+    return load().qk_kv_store(cache, k_ptr, k_tok, k_head, v_ptr, v_tok, v_head, n_tokens, table_ptr, ld_table,
+                              n_seqs, max_pages, seq_ptr, pos_ptr, stream)
+
+
+def qk_attn_decode(cache, q_ptr, q_seq, q_head, n_seqs, n_q_heads, table_ptr, ld_table, lens_ptr, max_len, scale,
+                   window, sinks, y_dtype, y_ptr, y_seq, y_head, workspace_ptr, workspace_bytes, stream=0):
+    """cache: a KVCacheDesc or None."""
+    return load().qk_attn_decode(cache, q_ptr, q_seq, q_head, n_seqs, n_q_heads, table_ptr, ld_table, lens_ptr,
+                                 max_len, scale, window, sinks, y_dtype, y_ptr, y_seq, y_head, workspace_ptr,
+                                 workspace_bytes, stream)
+
+
+def qk_attn_decode_workspace(cache, n_seqs, n_q_heads, max_len, window=0, sinks=0):
+    return load().qk_attn_decode_workspace(cache, n_seqs, n_q_heads, max_len, window, sinks)
+
+
+def qk_moe_route(logits_ptr, ldx, n_tokens, n_experts, n_used, score, bias_ptr, n_groups, topk_groups, group_top,
+                 renorm, scale, ids_ptr, ld_ids, weights_ptr, ldw, stream=0):
+    return load().qk_moe_route(logits_ptr, ldx, n_tokens, n_experts, n_used, score, bias_ptr, n_groups,
+                               topk_groups, group_top, renorm, scale, ids_ptr, ld_ids, weights_ptr, ldw, stream)
 
 
 # ---------------------------------------------------------------------------
@@ -334,3 +399,285 @@ def mul_mat(fmt, w, m, k, x, y=None, stream=None):
                     y.data_ptr(), y.stride(0), _stream(stream))
     _check(st, "qk_mul_mat")
     return y
+
+
+def mul_mat_vec_x8q(fmt, w, m, k, xq, y=None, stream=None):
+    """As mul_mat_vec_x8, over activations in 8 bits already: xq (n, >= k/32*36)
+    uint8, rows of 36-byte blocks as rms_norm(..., out_dtype="x8") gives them."""
+    import torch
+    _weight_check(fmt, w, m, k)
+    if not isinstance(xq, torch.Tensor) or xq.dtype != torch.uint8:
+        raise TypeError("xq must be a uint8 tensor of 8-bit activation blocks")
+    if xq.dim() == 1:
+        xq = xq.view(1, -1)
+    n = xq.shape[0]
+    if not 1 <= n <= 8:
+        raise ValueError(f"1..8 activation columns, got {n}")
+    _cols_check(xq, "xq", torch.uint8, n, k // 32 * X8_BLOCK_BYTES)
+    if y is None:
+        y = torch.empty((n, m), dtype=torch.float32, device=xq.device)
+    _cols_check(y, "y", torch.float32, n, m)
+    _same_device(w, xq, y)
+    st = qk_mul_mat_vec_x8q(fmt, w.data_ptr(), m, k, xq.data_ptr(), n, xq.stride(0), y.data_ptr(), y.stride(0),
+                            _stream(stream))
+    _check(st, "qk_mul_mat_vec_x8q")
+    return y
+
+
+def _row_stride(t):
+    """Stride of a tensor's first dimension, 0 where it has no second row."""
+    return t.stride(0) if t.shape[0] > 1 else 0
+
+
+def rms_norm(x, weight=None, eps=1e-5, residual=None, out_dtype="f32", y=None, residual_out=None, stream=None):
+    """Root-mean-square norm of the rows of x (n, k), fp32 or fp16, after
+    adding `residual` (as x): returns y, or (y, x + residual) with a residual.
+    out_dtype "f32", "f16", or "x8" (y uint8 (n, k/32*36), 8-bit activation
+    blocks for mul_mat_vec_x8q).  residual_out may be x or residual itself."""
+    import torch
+    types = {torch.float32: QK_F32, torch.float16: QK_F16}
+    if not isinstance(x, torch.Tensor) or x.dtype not in types:
+        raise TypeError("x must be a float32 or float16 tensor")
+    if x.dim() != 2 or x.shape[1] < 1:
+        raise ValueError(f"x must have shape (n, k) with k >= 1, got {tuple(x.shape)}")
+    outs = {"f32": (QK_F32, torch.float32), "f16": (QK_F16, torch.float16), "x8": (QK_X8, torch.uint8)}
+    if out_dtype not in outs:
+        raise ValueError(f"out_dtype must be 'f32', 'f16' or 'x8', got {out_dtype!r}")
+    n, k = x.shape
+    code, dt = outs[out_dtype]
+    if code == QK_X8 and k % 32 != 0:
+        raise ValueError(f"k must be a multiple of 32 for out_dtype 'x8', got {k}")
+    row = k // 32 * X8_BLOCK_BYTES if code == QK_X8 else k
+    _cols_check(x, "x", x.dtype, n, k)
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out without residual")
+    if residual is not None:
+        _cols_check(residual, "residual", x.dtype, n, k)
+        if residual_out is None:
+            residual_out = torch.empty((n, k), dtype=x.dtype, device=x.device)
+        _cols_check(residual_out, "residual_out", x.dtype, n, k)
+    if weight is not None:
+        if not isinstance(weight, torch.Tensor) or weight.dtype != torch.float32:
+            raise TypeError("weight must be a float32 tensor")
+        if weight.dim() != 1 or weight.shape[0] != k or weight.stride(0) != 1:
+            raise ValueError(f"weight must be a contiguous ({k},) tensor, got {tuple(weight.shape)}")
+    if y is None:
+        y = torch.empty((n, row), dtype=dt, device=x.device)
+    _cols_check(y, "y", dt, n, row)
+    _same_device(x, y, *[t for t in (residual, residual_out, weight) if t is not None])
+
+    def at(t):
+        return (0, 0) if t is None else (t.data_ptr(), t.stride(0))
+
+    st = qk_rms_norm(types[x.dtype], *at(x), *at(residual), at(weight)[0], float(eps), n, k, *at(residual_out), code,
+                     *at(y), _stream(stream))
+    _check(st, "qk_rms_norm")
+    return y if residual is None else (y, residual_out)
+
+
+class KVCache:
+    """A paged key-value cache over tensors that the caller keeps.
+
+    k, v: (n_pages, n_kv_heads, page_size, head_dim), float16, or int8 with
+    k_scale, v_scale float32 (n_pages, n_kv_heads, page_size): an element is
+    code * scale.  Any strides with contiguous rows, the same for k and v
+    (tokens outside heads: pass a view transposed to this order)."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        if not isinstance(k, torch.Tensor) or not isinstance(v, torch.Tensor) or k.dtype != v.dtype \
+                or k.dtype not in (torch.float16, torch.int8):
+            raise TypeError("k and v must be float16 or int8 tensors")
+        if k.dim() != 4 or k.shape != v.shape or min(k.shape) < 1:
+            raise ValueError("k and v must both be (n_pages, n_kv_heads, page_size, head_dim), "
+                             f"got {tuple(k.shape)} and {tuple(v.shape)}")
+        i8 = k.dtype == torch.int8
+        pages, heads, page, dim = k.shape
+        if dim % 32 != 0 or dim > 256:
+            raise ValueError(f"head_dim must be a multiple of 32 up to 256, got {dim}")
+
+        def strides(t, n):
+            return [t.stride(i) if t.shape[i] > 1 else 0 for i in range(n)]
+
+        if k.stride(3) != 1 or v.stride(3) != 1 or strides(k, 3) != strides(v, 3):
+            raise ValueError("k and v must have contiguous rows and the same strides")
+        if any(s * k.element_size() % 16 for s in strides(k, 3)) or k.data_ptr() % 16 or v.data_ptr() % 16:
+            raise ValueError("rows of k and v must begin at multiples of 16 bytes")
+        if i8 != (k_scale is not None) or i8 != (v_scale is not None):
+            raise ValueError("k_scale and v_scale belong to int8 caches, and only to them")
+        sc = [0, 0, 0]
+        if i8:
+            for t in (k_scale, v_scale):
+                if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
+                    raise TypeError("k_scale and v_scale must be float32 tensors")
+                if tuple(t.shape) != (pages, heads, page):
+                    raise ValueError(f"k_scale and v_scale must be ({pages}, {heads}, {page}), got {tuple(t.shape)}")
+            sc = strides(k_scale, 3)
+            if strides(v_scale, 3) != sc:
+                raise ValueError("k_scale and v_scale must have the same strides")
+        _same_device(k, v, *([k_scale, v_scale] if i8 else []))
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.n_heads, self.page_size, self.head_dim = pages, heads, page, dim
+        self.device = k.device
+        self.desc = KVCacheDesc(QK_KV_I8 if i8 else QK_KV_F16, k.data_ptr(), v.data_ptr(),
+                                k_scale.data_ptr() if i8 else None, v_scale.data_ptr() if i8 else None,
+                                pages, heads, page, dim, *strides(k, 3), *sc)
+
+    @classmethod
+    def empty(cls, n_pages, n_heads, page_size, head_dim, dtype="f16", device="cuda"):
+        """A cache of its own tensors; dtype "f16" or "i8"."""
+        import torch
+        if dtype not in ("f16", "i8"):
+            raise ValueError(f"dtype must be 'f16' or 'i8', got {dtype!r}")
+        shape = (n_pages, n_heads, page_size, head_dim)
+        kv = [torch.zeros(shape, dtype=torch.float16 if dtype == "f16" else torch.int8, device=device)
+              for _ in range(2)]
+        if dtype == "i8":
+            kv += [torch.zeros(shape[:3], dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*kv)
+
+
+def _int32_check(t, name, dim):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+        raise TypeError(f"{name} must be an int32 tensor")
+    if t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be {dim}-dimensional with contiguous rows, got {tuple(t.shape)}")
+
+
+def _heads_check(t, name, dtype, n, heads, dim):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor")
+    if tuple(t.shape) != (n, heads, dim) or (n > 0 and t.stride(2) != 1):
+        raise ValueError(f"{name} must have shape ({n}, {heads}, {dim}) with contiguous rows, got {tuple(t.shape)}")
+
+
+def kv_store(cache, k, v, table, pos, seq=None, stream=None):
+    """Write new keys and values into a paged cache: token i of k and v
+    (n_tokens, n_kv_heads, head_dim) fp32 goes to position pos[i] of sequence
+    seq[i] (i itself without seq), whose pages are table[seq[i]].  table int32
+    (n_seqs, max_pages); pos, seq int32 (n_tokens,).  A token with no place in
+    the table or the pool is left out."""
+    import torch
+    _int32_check(table, "table", 2)
+    _int32_check(pos, "pos", 1)
+    n = pos.shape[0]
+    if seq is not None:
+        _int32_check(seq, "seq", 1)
+        if seq.shape[0] != n:
+            raise ValueError(f"seq has {seq.shape[0]} tokens, pos {n}")
+    elif table.shape[0] < n:
+        raise ValueError(f"table has {table.shape[0]} sequences for {n} tokens")
+    for t, name in ((k, "k"), (v, "v")):
+        _heads_check(t, name, torch.float32, n, cache.n_heads, cache.head_dim)
+    _same_device(cache.k, k, v, table, pos, *([seq] if seq is not None else []))
+    st = qk_kv_store(cache.desc, k.data_ptr(), _row_stride(k), k.stride(1) if cache.n_heads > 1 else 0,
+                     v.data_ptr(), _row_stride(v), v.stride(1) if cache.n_heads > 1 else 0,
+                     n, table.data_ptr(), table.stride(0), table.shape[0], table.shape[1],
+                     seq.data_ptr() if seq is not None else None, pos.data_ptr(), _stream(stream))
+    _check(st, "qk_kv_store")
+
+
+def attn_decode_workspace(cache, n_seqs, n_q_heads, max_len, window=0, sinks=0):
+    """Scratch for attn_decode calls of these sizes: a uint8 tensor, or None
+    where none is needed.  One tensor serves one stream at a time."""
+    import torch
+    need = qk_attn_decode_workspace(cache.desc, n_seqs, n_q_heads, max_len, window, sinks)
+    return torch.empty(need, dtype=torch.uint8, device=cache.device) if need else None
+
+
+def attn_decode(cache, q, table, lens, scale=None, window=0, sinks=0, max_len=None, out_dtype="f32", y=None,
+                workspace=None, stream=None):
+    """Attention of one new token per sequence over a paged cache.  q (n_seqs,
+    n_q_heads, head_dim) fp32; table int32 (n_seqs, max_pages); lens int32
+    (n_seqs,), the new token counted.  scale: 1/sqrt(head_dim) unless given.
+    window > 0: the last `window` tokens and the first `sinks` are seen.
+    max_len bounds the lengths (default: all of the table's pages) and sizes
+    the split over the cache; a length above it gives NaN.  Returns y (n_seqs,
+    n_q_heads, head_dim), fp32 or (out_dtype "f16") fp16."""
+    import torch
+    if out_dtype not in ("f32", "f16"):
+        raise ValueError(f"out_dtype must be 'f32' or 'f16', got {out_dtype!r}")
+    code, dt = {"f32": (QK_F32, torch.float32), "f16": (QK_F16, torch.float16)}[out_dtype]
+    _int32_check(table, "table", 2)
+    _int32_check(lens, "lens", 1)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise TypeError("q must be a float32 tensor (n_seqs, n_q_heads, head_dim)")
+    n, heads, dim = q.shape[0], q.shape[1], cache.head_dim
+    _heads_check(q, "q", torch.float32, n, heads, dim)
+    if heads < 1 or heads % cache.n_heads != 0:
+        raise ValueError(f"{heads} query heads over {cache.n_heads} key-value heads")
+    if table.shape[0] != n or lens.shape[0] != n:
+        raise ValueError(f"q has {n} sequences, table {table.shape[0]}, lens {lens.shape[0]}")
+    room = table.shape[1] * cache.page_size
+    max_len = room if max_len is None else int(max_len)
+    if not 1 <= max_len <= room:
+        raise ValueError(f"max_len {max_len}: the table has room for {room} tokens")
+    if window < 0 or sinks < 0:
+        raise ValueError("window and sinks must not be negative")
+    if y is None:
+        y = torch.empty((n, heads, dim), dtype=dt, device=q.device)
+    _heads_check(y, "y", dt, n, heads, dim)
+    need = qk_attn_decode_workspace(cache.desc, n, heads, max_len, window, sinks)
+    handle = _stream(stream)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        if handle != torch.cuda.current_stream(q.device).cuda_stream:
+            # not to be given out again before the other stream is done with it
+            workspace.record_stream(torch.cuda.ExternalStream(handle, device=q.device))
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise TypeError("workspace must be a contiguous uint8 tensor")
+        if workspace.numel() < need:
+            raise ValueError(f"workspace holds {workspace.numel()} bytes, {need} are needed")
+    _same_device(cache.k, q, table, lens, y, *([workspace] if workspace is not None else []))
+    st = qk_attn_decode(cache.desc, q.data_ptr(), _row_stride(q), q.stride(1) if heads > 1 else 0, n, heads,
+                        table.data_ptr(), table.stride(0), lens.data_ptr(), max_len,
+                        dim ** -0.5 if scale is None else float(scale), window, sinks, code, y.data_ptr(),
+                        _row_stride(y), y.stride(1) if heads > 1 else 0,
+                        workspace.data_ptr() if workspace is not None else None, need, handle)
+    _check(st, "qk_attn_decode")
+    return y
+
+
+def moe_route(logits, n_used, score="softmax", bias=None, n_groups=1, topk_groups=1, group_top=1, renorm=True,
+              scale=1.0, ids=None, weights=None, stream=None):
+    """Choose n_used experts for each token from logits (n_tokens, n_experts)
+    fp32: (ids int32, weights fp32), both (n_tokens, n_used), the ids as
+    mul_mat_vec_id takes them.  score "softmax" or "sigmoid"; bias
+    (n_experts,) fp32 is added for the choice only; with n_groups > 1 only the
+    topk_groups best groups of neighbouring experts take part, by the sum of
+    their group_top (1 or 2) largest values."""
+    import torch
+    scores = {"softmax": QK_SOFTMAX, "sigmoid": QK_SIGMOID}
+    if score not in scores:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+    if not isinstance(logits, torch.Tensor) or logits.dtype != torch.float32:
+        raise TypeError("logits must be a float32 tensor")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError(f"logits must be (n_tokens, n_experts) with contiguous rows, got {tuple(logits.shape)}")
+    n, experts = logits.shape
+    if bias is not None:
+        if not isinstance(bias, torch.Tensor) or bias.dtype != torch.float32:
+            raise TypeError("bias must be a float32 tensor")
+        if bias.dim() != 1 or bias.shape[0] != experts or bias.stride(0) != 1:
+            raise ValueError(f"bias must be a contiguous ({experts},) tensor, got {tuple(bias.shape)}")
+    if not 1 <= n_used <= 64:
+        raise ValueError(f"n_used must be 1..64, got {n_used}")
+    if ids is None:
+        ids = torch.empty((n, n_used), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((n, n_used), dtype=torch.float32, device=logits.device)
+    for t, name, dt in ((ids, "ids", torch.int32), (weights, "weights", torch.float32)):
+        if not isinstance(t, torch.Tensor) or t.dtype != dt:
+            raise TypeError(f"{name} must be a {dt} tensor")
+        if tuple(t.shape) != (n, n_used) or (n_used > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name} must have shape ({n}, {n_used}) with contiguous rows, got {tuple(t.shape)}")
+    _same_device(logits, ids, weights, *([bias] if bias is not None else []))
+    st = qk_moe_route(logits.data_ptr(), logits.stride(0), n, experts, n_used, scores[score],
+                      bias.data_ptr() if bias is not None else None, n_groups, topk_groups, group_top, int(renorm),
+                      float(scale), ids.data_ptr(), ids.stride(0), weights.data_ptr(), weights.stride(0),
+                      _stream(stream))
+    _check(st, "qk_moe_route")
+    return ids, weights

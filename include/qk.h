@@ -1,6 +1,7 @@
 /*
  * qk.h - C ABI of libqk: ggml block-quantized dequantize, GEMV and GEMM on
- * AMD gfx950 (MI355X).
+ * AMD gfx950 (MI355X), and what a decode step has between them: RMS norm,
+ * paged key-value cache and its attention, routing to experts.
  *
  * Block formats (32 weights per block, little-endian binary16 fields, blocks
  * packed back to back, a matrix stored row after row with k/32 blocks per row
@@ -59,10 +60,25 @@ enum qk_format {
     QK_Q5_1 = 5
 };
 
-/* Output element types of qk_dequantize. */
+/* Element types.  QK_X8: blocks of 32 values in 36 bytes, an fp32 scale d and
+ * then 32 int8 codes q, value d*q; rows of k/32 blocks back to back.  An output
+ * of qk_rms_norm and the input of qk_mul_mat_vec_x8q only. */
 enum qk_dtype {
     QK_F32 = 0,
-    QK_F16 = 1
+    QK_F16 = 1,
+    QK_X8 = 2
+};
+
+/* Element types of a key-value cache. */
+enum qk_kv_type {
+    QK_KV_F16 = 0,
+    QK_KV_I8 = 1    /* int8 codes, one fp32 scale per token and head */
+};
+
+/* Scores of qk_moe_route. */
+enum qk_score {
+    QK_SOFTMAX = 0,
+    QK_SIGMOID = 1
 };
 
 /* Status codes. */
@@ -167,6 +183,22 @@ int qk_mul_mat_vec_x8(int fmt, const void *w, int64_t m, int64_t k,
                       const float *x, int64_t n, int64_t ldx,
                       float *y, int64_t ldy, void *stream);
 
+/*
+ * qk_mul_mat_vec_x8q - qk_mul_mat_vec_x8 over activations that are in 8 bits
+ * already: x is n columns of k/32 QK_X8 blocks (fp32 scale, 32 int8 codes),
+ * as qk_rms_norm writes them.  With the blocks that qk_mul_mat_vec_x8 makes
+ * of the same activations the outputs are the same, bit for bit; several
+ * products of one vector then share one quantization.  Any scale and codes
+ * -128..127 are taken.
+ *
+ *   xq         QK_X8 blocks, 4-byte aligned; column j starts at byte j*ldx
+ *   ldx        bytes, a multiple of 4, >= k/32*36 (ignored if n == 1)
+ * Other arguments, layouts and errors as qk_mul_mat_vec (n = 0..8).
+ */
+int qk_mul_mat_vec_x8q(int fmt, const void *w, int64_t m, int64_t k,
+                       const void *xq, int64_t n, int64_t ldx,
+                       float *y, int64_t ldy, void *stream);
+
 /* One problem of a grouped GEMV: y = W x (layout as in qk_mul_mat_vec). */
 typedef struct qk_mat_vec_item {
     const void *w;      /* m rows of k/32 blocks, 2-byte aligned */
@@ -265,6 +297,167 @@ int qk_mul_mat_vec_id(int fmt, const void *w, int64_t n_experts, int64_t expert_
 int qk_mul_mat(int fmt, const void *w, int64_t m, int64_t k,
                const void *x_f16, int64_t n, int64_t ldx,
                float *y, int64_t ldy, void *stream);
+
+/*
+ * qk_rms_norm - root-mean-square norm of n rows, with the residual's addition.
+ *
+ *   s[j][c] = x[j][c] + residual[j][c]                  (fp32)
+ *   sum[j][c] = s[j][c]                                 (rounded to x_dtype)
+ *   y[j][c] = s[j][c] / sqrt(mean_c(s[j][c]^2) + eps) * weight[c]
+ *
+ * The norm takes s before it is rounded.  The mean is held in fp64 and the
+ * factor rounded to fp32 once; y is two more roundings, and one to its type.
+ * QK_X8 outputs quantize each 32-element block of y to codes
+ * q = round-half-even(y / d) with the scale rule of qk_mul_mat_vec_x8 (d a
+ * power of two; 0 for an all-zero block; NaN, with codes 0, for a block that
+ * holds an infinite or NaN value).
+ *
+ *   x_dtype    QK_F32 or QK_F16: x, residual and sum
+ *   x          n rows of k elements, stride ldx >= k elements
+ *   residual   as x (stride ldr), or NULL for none
+ *   weight     fp32[k], or NULL for ones
+ *   eps        >= 0
+ *   k          >= 1, at most 2^30; a multiple of 32 for QK_X8 outputs
+ *   sum        as x (stride lds), or NULL to leave it out; may be x or
+ *              residual itself (the same pointer and stride)
+ *   y_dtype    QK_F32, QK_F16 or QK_X8
+ *   y          n rows; stride ldy in elements (>= k), for QK_X8 in bytes
+ *              (>= k/32*36, a multiple of 4)
+ * Strides are ignored if n == 1.  Pointers aligned to their element size.
+ */
+int qk_rms_norm(int x_dtype, const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                const float *weight, double eps, int64_t n, int64_t k,
+                void *sum, int64_t lds, int y_dtype, void *y, int64_t ldy, void *stream);
+
+/*
+ * A paged key-value cache.  Token `slot` of page `p` has, for key-value head
+ * h, head_dim contiguous elements starting at element
+ * p*page_stride + h*head_stride + slot*slot_stride of k (keys) and of v
+ * (values), so that heads may lie outside or inside tokens.  Which pages hold
+ * a sequence is told by a page table (device int32): token t of sequence s is
+ * slot t % page_size of page table[s*ld_table + t / page_size].
+ * QK_KV_I8: an element is code * scale, the scale of a token and head at
+ * element p*scale_page_stride + h*scale_head_stride + slot*scale_slot_stride
+ * of k_scale and of v_scale.
+ * The struct is read during the call only; the pools are the caller's.
+ */
+typedef struct qk_kv_cache {
+    int type;               /* enum qk_kv_type */
+    void *k, *v;            /* 16-byte aligned pools */
+    float *k_scale, *v_scale;   /* QK_KV_I8 (else ignored) */
+    int64_t n_pages;        /* 1..INT32_MAX */
+    int64_t n_heads;        /* key-value heads, 1..65535 */
+    int64_t page_size;      /* tokens per page, 1..2^20 */
+    int64_t head_dim;       /* a multiple of 32 from 32 to 256 */
+    int64_t page_stride, head_stride, slot_stride;   /* elements; multiples of 16 bytes; >= 0 */
+    int64_t scale_page_stride, scale_head_stride, scale_slot_stride;   /* elements; >= 0 */
+} qk_kv_cache;
+
+/*
+ * qk_kv_store - write the keys and values of new tokens into a paged cache.
+ *
+ *   token i goes to position pos[i] of sequence seq[i]
+ *
+ * QK_KV_F16: rounded to nearest even (overflow to infinity).  QK_KV_I8: per
+ * token and head, scale d = max|x| / 127 and codes round-half-even(x / d),
+ * both divisions rounded to fp32 (d = 0 and codes 0 where that is 0; d = NaN
+ * and codes 0 where a value is infinite or NaN).
+ * A token is left out, and nothing written for it, if its sequence or
+ * position is outside the table or its page id outside the pool.  Two tokens
+ * of one call must not have the same place.
+ *
+ *   k, v       fp32; token i, head h at element i*k_tok + h*k_head
+ *              (v_tok, v_head), head_dim contiguous elements; strides >= 0
+ *   n_tokens   >= 0 (0 is a no-op); 2*n_tokens*n_heads <= INT32_MAX
+ *   table      device int32, n_seqs rows of max_pages ids, stride ld_table
+ *   seq        device int32[n_tokens], or NULL: token i is of sequence i
+ *   pos        device int32[n_tokens]
+ * Errors: QK_ERR_INVALID_ARG also where rows of the pools overlap.
+ */
+int qk_kv_store(const qk_kv_cache *cache, const float *k, int64_t k_tok, int64_t k_head,
+                const float *v, int64_t v_tok, int64_t v_head, int64_t n_tokens,
+                const int32_t *table, int64_t ld_table, int64_t n_seqs, int64_t max_pages,
+                const int32_t *seq, const int32_t *pos, void *stream);
+
+/*
+ * qk_attn_decode - attention of one new token per sequence over a paged cache.
+ *
+ *   z_t = scale * q . K_t    for the tokens t < lens[s] that the query sees
+ *   y   = sum_t exp(z_t) V_t / sum_t exp(z_t)
+ *
+ * Query head h of n_q_heads takes key-value head h / (n_q_heads / n_heads).
+ * With window > 0 the query (the token at lens[s] - 1) sees the last `window`
+ * tokens and the first `sinks`; with window == 0 all of them.  Tokens that
+ * are not seen are not used, whatever their pages hold, and table entries of
+ * pages without a token that is seen are not followed.
+ * lens[s] <= 0: zeros.  NaN: lens[s] above max_len, or a page id outside the
+ * pool.  The result does not depend on other sequences, and is the same on
+ * every run.
+ * Products are taken in fp16 high and low parts with fp32 sums: the error is
+ * that of fp32 arithmetic.
+ *
+ *   q          fp32; sequence s, head h at element s*q_seq + h*q_head,
+ *              head_dim contiguous elements; strides >= 0
+ *   n_seqs     >= 0 (0 is a no-op)
+ *   n_q_heads  a multiple of the cache's n_heads
+ *   table      device int32, n_seqs rows, stride ld_table >= the pages of
+ *              max_len tokens (ignored if n_seqs == 1)
+ *   lens       device int32[n_seqs]: tokens in the cache, the new one among them
+ *   max_len    1..2^30, no length is above it
+ *   window, sinks   >= 0
+ *   y_dtype    QK_F32 or QK_F16; y laid out as q with y_seq, y_head; the rows
+ *              must not overlap
+ *   workspace  device memory, 16-byte aligned, of the bytes that
+ *              qk_attn_decode_workspace gives for the same arguments (NULL if
+ *              0); it need not be cleared, and is free for other use once the
+ *              enqueued work is done
+ */
+int qk_attn_decode(const qk_kv_cache *cache, const float *q, int64_t q_seq, int64_t q_head,
+                   int64_t n_seqs, int64_t n_q_heads, const int32_t *table, int64_t ld_table,
+                   const int32_t *lens, int64_t max_len, float scale, int64_t window, int64_t sinks,
+                   int y_dtype, void *y, int64_t y_seq, int64_t y_head,
+                   void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that qk_attn_decode needs; 0 where it needs none, and on
+ * a bad argument. */
+size_t qk_attn_decode_workspace(const qk_kv_cache *cache, int64_t n_seqs, int64_t n_q_heads,
+                                int64_t max_len, int64_t window, int64_t sinks);
+
+/*
+ * qk_moe_route - choose experts for tokens: the ids that qk_mul_mat_vec_id
+ * takes, and their weights.
+ *
+ *   score = softmax or sigmoid of the token's logits (over all experts)
+ *   value = score + bias          (bias decides the choice only)
+ *   with n_groups > 1, experts outside the topk_groups best groups are left
+ *   out; a group is n_experts/n_groups neighbours, its value the sum of its
+ *   group_top (1 or 2) largest values
+ *   ids[t][i] = the expert with the i-th largest value, i < n_used
+ *   weights[t][i] = score of that expert, over the sum of the n_used with
+ *   renorm != 0, times scale
+ *
+ * Equal values: the lowest index first (groups too).  Without a bias and with
+ * group_top == 1 the logits are compared, which both scores rise with; else
+ * the fp32 values, whose softmax sum is held in fp64 and rounded once, so that
+ * the choice does not hang on the order of a sum.  A NaN value comes last.
+ * The ids of a token are always n_used different experts.  Scores of a row
+ * of -infinity alone are 0 under softmax; weights whose sum is 0 are 0 with
+ * renorm.
+ *
+ *   logits     fp32, n_tokens rows of n_experts, stride ldx >= n_experts
+ *   n_experts  1..1024
+ *   n_used     1..64, at most topk_groups * (n_experts / n_groups)
+ *   score      QK_SOFTMAX or QK_SIGMOID
+ *   bias       fp32[n_experts], or NULL for none
+ *   n_groups   1..64, divides n_experts; topk_groups 1..n_groups
+ *   ids        int32, stride ld_ids >= n_used
+ *   weights    fp32, stride ldw >= n_used
+ * Strides are ignored if n_tokens == 1; n_tokens == 0 is a no-op.
+ */
+int qk_moe_route(const float *logits, int64_t ldx, int64_t n_tokens, int64_t n_experts,
+                 int64_t n_used, int score, const float *bias, int64_t n_groups,
+                 int64_t topk_groups, int64_t group_top, int renorm, float scale,
+                 int32_t *ids, int64_t ld_ids, float *weights, int64_t ldw, void *stream);
 
 #ifdef __cplusplus
 }
