@@ -8,21 +8,24 @@
 //
 // The matrix cores do both products.  A wave takes 32 tokens (two sub-tiles
 // of 16) and up to 16 query heads that share the key-value head:
-//   S^T (tokens x heads) = K Q^T,  O^T (dims x heads) += V^T P^T,
-// with v_mfma_f32_16x16x32_f16.  The result of the first has in lane
-// (g = lane / 16, j = lane % 16) head j and tokens 4g..4g+3 of each sub-tile,
-// which is the second's right operand as it stands (the order of the summed
-// tokens is free as long as V uses the same), so the probabilities never
-// leave their registers.  V is read row by row, lane (g, j) taking dims
-// j*D/16 .. of its eight tokens, and a byte permute pairs tokens into the
-// left operand.  All of a lane's softmax state belongs to its head j.
+//   S^T (tokens x heads) = K Q^T,  O^T (dims x heads) += V^T P^T.
+// The result of the first has in lane (g = lane / 16, j = lane % 16) head j
+// and tokens 4g..4g+3 of each sub-tile, which is the second's right operand
+// as it stands (the order of the summed tokens is free as long as V uses the
+// same), so the probabilities never leave their registers.  V is read row by
+// row, lane (g, j) taking dims j*D/16 .. of its eight tokens.  All of a lane's
+// softmax state belongs to its head j.
 //
-// fp16 keys and values are exact operands.  q and p are not: each is split
-// into a high and a low fp16 part (two products, about 22 bits), q scaled by
-// a power of two to a largest magnitude of 2^13..2^14 and p by 2^14, so that
-// the parts' absolute precision is 2^-38 of the largest.  8-bit keys and
-// values are whole numbers, exact in fp16; the key's scale multiplies z, the
-// value's multiplies p (relative to the largest met so far).
+// Scores: v_mfma_f32_16x16x32_f16.  fp16 keys and 8-bit codes are exact
+// operands; q is split into a high and a low fp16 part (two products, about
+// 22 bits), scaled by a power of two to a largest magnitude of 2^13..2^14, so
+// that the parts' absolute precision is 2^-38 of the row's largest.
+// Outputs: a probability may be tiny and still decide an output (where the
+// likely tokens have value 0), so it keeps its 24 bits and its exponent.
+// fp16 values: v_mfma_f32_16x16x4_f32, which takes p as it is.  8-bit values:
+// codes are exact in bf16 and p times the value's scale is split into three
+// bf16 parts, v_mfma_f32_16x16x32_bf16; the 8-bit cache has half the bytes
+// per product, too few to hide the fp32 form's time.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -35,13 +38,13 @@
 namespace qk {
 
 typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 b8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
 typedef float f4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
 
 constexpr float kAttnLow = -3.402823466e38f;  // the running maximum before any token
-constexpr float kAttnPexp = 14.0f;            // probabilities are held times 2^14
 
 // Largest / sum of the four lanes that share lane % 16, to all of them.
 __device__ __forceinline__ float quad_rows_max(float v) {
@@ -72,6 +75,27 @@ __device__ __forceinline__ void split8(const float (&p)[8], h8_t &hi, h8_t &lo) 
     lo = __builtin_bit_cast(h8_t, l);
 }
 
+// Three bf16 parts of eight values, each the leading 8 bits of what is left:
+// together all 24 bits.
+__device__ __forceinline__ void split8_bf16(const float (&p)[8], b8_t (&part)[3]) {
+    uint32_t r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = __builtin_bit_cast(uint32_t, p[i]);
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+        u4_t w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_perm(r[2 * i + 1], r[2 * i], 0x07060302u);
+        part[n] = __builtin_bit_cast(b8_t, w);
+        if (n < 2) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                r[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, r[i]) -
+                                                        __builtin_bit_cast(float, r[i] & 0xFFFF0000u));
+        }
+    }
+}
+
 // Two bytes b, held as code + 128 in the low halves of a dword's 16-bit words
 // (fp16 subnormals b * 2^-24), to fp16 code * 2^-9: exact.
 __device__ __forceinline__ uint32_t codes_f16(uint32_t w) {
@@ -80,7 +104,6 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t w) {
     const h2_t o = {(_Float16)-0.25f, (_Float16)-0.25f};
     return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(x, c, o));
 }
-constexpr float kCodeUnit = 512.0f;  // 2^9
 
 // Eight int8 codes to fp16 code * 2^-9.
 __device__ __forceinline__ h8_t codes8_f16(uint32_t w0, uint32_t w1) {
@@ -299,7 +322,6 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
 #pragma unroll
     for (int c = 0; c < DPL; ++c) o[c] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
     float m = kAttnLow, l = 0.0f;
-    float vtop = 0.0f, vinv = 0.0f;  // power of two at or above the value scales met (8 bits), its inverse
 
     float s[8];  // scores of tokens 4g + i (0..3) and 16 + 4g + i (4..7), in log2
     auto scores = [&]() __attribute__((always_inline)) {
@@ -326,8 +348,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
             }
         }
     };
-    h8_t ph, pl;
-    // p from s, in place of what s was; the value scales go into ph and pl
+    float p[8];  // probabilities relative to 2^m, with 8-bit values times their scales
     auto probabilities = [&](int v) __attribute__((always_inline)) {
         const int t0 = tile_t0(v);
         const bool whole = t0 + kAttnTile <= sp.len && (t0 >= sp.ws || t0 + kAttnTile <= a.sinks);
@@ -343,50 +364,30 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
 #pragma unroll
         for (int i = 1; i < 8; ++i) top = fmaxf(top, s[i]);
         top = quad_rows_max(top);
-        float vt = 0.0f;
-        if constexpr (I8) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (!whole) vr.sc[i] = mask >> i & 1 ? vr.sc[i] : 0.0f;
-                vt = fmaxf(vt, fabsf(vr.sc[i]));
-            }
-            vt = quad_rows_max(vt);
-        }
-        if (__any(top > m || (I8 && vt > vtop))) {
+        if (__any(top > m)) {
             const float mn = fmaxf(m, top);
-            float f = __builtin_amdgcn_exp2f(m - mn);
+            const float f = __builtin_amdgcn_exp2f(m - mn);
             l *= f;
             m = mn;
-            if constexpr (I8) {
-                if (vt > vtop) {
-                    int ex;
-                    (void)frexpf(vt, &ex);
-                    const float vn = ldexpf(1.0f, min(ex, 127));
-                    vinv = 1.0f / vn;
-                    f *= vtop * vinv;
-                    vtop = vn;
-                }
-            }
 #pragma unroll
             for (int c = 0; c < DPL; ++c)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[c][i] *= f;
         }
-        const float mp = m - kAttnPexp;
-        float p[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            p[i] = __builtin_amdgcn_exp2f(s[i] - mp);
+            p[i] = __builtin_amdgcn_exp2f(s[i] - m);
             if (!whole) p[i] = mask >> i & 1 ? p[i] : 0.0f;
             l += p[i];
         }
         if constexpr (I8) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] *= vr.sc[i] * vinv;
-        }
-        split8(p, ph, pl);
-        // rows that are not seen may hold anything, NaN included
-        if (!whole) {
+            for (int i = 0; i < 8; ++i) {
+                p[i] *= vr.sc[i];
+                if (!whole) p[i] = mask >> i & 1 ? p[i] : 0.0f;
+            }
+        } else if (!whole) {
+            // rows that are not seen may hold anything, NaN included
 #pragma unroll
             for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -394,24 +395,31 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
         }
     };
     auto outputs = [&]() __attribute__((always_inline)) {
+        if constexpr (I8) {
+            b8_t part[3];
+            split8_bf16(p, part);
 #pragma unroll
-        for (int c = 0; c < DPL; ++c) {
-            u4_t x;
+            for (int c = 0; c < DPL; ++c) {
+                u4_t x;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (I8) {
-                    const uint32_t e0 = vr.w[2 * i].w[c / 4], e1 = vr.w[2 * i + 1].w[c / 4];
-                    // byte c % 4 of both, moved from code to code + 128
-                    const uint32_t sel = 0x0c000c00u | (uint32_t)(c % 4) | ((uint32_t)(c % 4 + 4) << 16);
-                    x[i] = codes_f16(__builtin_amdgcn_perm(e1, e0, sel) ^ 0x00800080u);
-                } else {
-                    const uint32_t e0 = vr.w[2 * i].w[c / 2], e1 = vr.w[2 * i + 1].w[c / 2];
-                    x[i] = __builtin_amdgcn_perm(e1, e0, c % 2 ? 0x07060302u : 0x05040100u);
+                for (int i = 0; i < 4; ++i) {
+                    const float e0 = (float)(int8_t)(vr.w[2 * i].w[c / 4] >> (8 * (c % 4)));
+                    const float e1 = (float)(int8_t)(vr.w[2 * i + 1].w[c / 4] >> (8 * (c % 4)));
+                    x[i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, e1), __builtin_bit_cast(uint32_t, e0),
+                                                 0x07060302u);
                 }
+                const b8_t vv = __builtin_bit_cast(b8_t, x);
+#pragma unroll
+                for (int n = 0; n < 3; ++n) o[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, part[n], o[c], 0, 0, 0);
             }
-            const h8_t vv = __builtin_bit_cast(h8_t, x);
-            o[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, ph, o[c], 0, 0, 0);
-            o[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, pl, o[c], 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int c = 0; c < DPL; ++c) {
+                    const h2_t x = __builtin_bit_cast(h2_t, vr.w[i].w[c / 2]);
+                    o[c] = __builtin_amdgcn_mfma_f32_16x16x4f32((float)x[c % 2], p[i], o[c], 0, 0, 0);
+                }
         }
     };
 
@@ -440,7 +448,6 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
     if (__any(bad)) l = __builtin_nanf("");
 
     // join the waves
-    const float unit = I8 ? vtop * kCodeUnit : 1.0f;
     if (g == 0) {
         sm[wave][j][0] = m;
         sm[wave][j][1] = l;
@@ -449,7 +456,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int c = 0; c < DPL; ++c) so[wave][j][(4 * g + i) * DPL + c] = o[c][i] * unit;
+            for (int c = 0; c < DPL; ++c) so[wave][j][(4 * g + i) * DPL + c] = o[c][i];
     }
     __syncthreads();
     for (int i = threadIdx.x; i < nh * (D / 4); i += 64 * kAttnWaves) {
