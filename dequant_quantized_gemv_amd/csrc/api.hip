@@ -121,6 +121,9 @@ Ranges cache_ranges(const qk_kv_cache &c) {
     return out;
 }
 
+#ifndef QK_ATTN_WG_PER_CU
+#define QK_ATTN_WG_PER_CU 4
+#endif
 // Sizes and the split of a decode attention over the cache's length: the
 // tokens of a sequence go to workgroups in chunks of `chunk_tiles` 32-token
 // tiles.  The lengths are on the device, so the chunk follows from max_len:
@@ -138,7 +141,12 @@ int attn_plan(const qk_kv_cache &c, int64_t n_seqs, int64_t n_q_heads, int64_t m
     a.head_tiles = (a.group + qk::kAttnHeads - 1) / qk::kAttnHeads;
     a.n_pages = (int)c.n_pages;
     a.page_size = (int)c.page_size;
-    a.page_shift = (c.page_size & (c.page_size - 1)) == 0 ? __builtin_ctzll((unsigned long long)c.page_size) : -1;
+    // quotients of 30-bit numbers: with 2^s >= page_size, the product's excess
+    // over t * 2^(30+s) / page_size stays below 2^(30+s) / page_size
+    int s = 0;
+    while ((int64_t(1) << s) < c.page_size) ++s;
+    a.page_shift = 30 + s;
+    a.page_magic = (uint32_t)(((uint64_t(1) << (30 + s)) + c.page_size - 1) / c.page_size);
     a.max_len = (int)max_len;
     a.window = (int)std::min<int64_t>(window, max_len);
     a.sinks = (int)std::min<int64_t>(sinks, max_len);
@@ -149,7 +157,7 @@ int attn_plan(const qk_kv_cache &c, int64_t n_seqs, int64_t n_q_heads, int64_t m
         tiles = std::min<int64_t>(tiles, (a.sinks + qk::kAttnTile - 1) / qk::kAttnTile +
                                              (a.window + qk::kAttnTile - 1) / qk::kAttnTile + 1);
     const int64_t rows = n_seqs * a.n_kv * a.head_tiles;
-    const int64_t target = 4 * (int64_t)qk::device_cus();
+    const int64_t target = QK_ATTN_WG_PER_CU * (int64_t)qk::device_cus();
     int64_t chunk = (tiles * rows + target - 1) / target;
     chunk = std::max<int64_t>(qk::kAttnWaves, (chunk + qk::kAttnWaves - 1) / qk::kAttnWaves * qk::kAttnWaves);
     a.chunk_tiles = (int)std::min<int64_t>(chunk, tiles);

@@ -24,7 +24,8 @@ struct AttnArgs {
     int64_t q_seq, q_head, y_seq, y_head;            // elements
     int64_t ld_table;
     int n_seqs, n_heads, n_kv, group, head_tiles;
-    int n_pages, page_size, page_shift;              // page_shift: log2(page_size), or -1
+    int n_pages, page_size;
+    uint32_t page_magic, page_shift;                 // t / page_size == t * page_magic >> page_shift, t < 2^30
     int max_len, window, sinks;
     int chunk_tiles, nchunks;
     float qscale;                  // softmax scale * log2(e)

@@ -126,7 +126,8 @@ __device__ __forceinline__ Bytes<N> load_bytes(const uint8_t *p) {
 
 // TILED: a page holds whole sub-tiles (page_size a multiple of 16) and scales
 // of neighbouring tokens lie side by side, so a sub-tile's page is looked up
-// once, in scalar registers; otherwise every lane looks up its own tokens.
+// once, in scalar registers.  Otherwise lane l finds the row (and reads the
+// scales) of the tile's token l % 32, and lanes take them from one another.
 template <int D, bool I8, bool TILED>
 __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode_kernel(const AttnArgs a) {
     constexpr int ES = I8 ? 1 : 2;         // bytes of a key or value element
@@ -211,39 +212,50 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
     // a token that is seen in the tile at t0
     auto seen_in = [&](int t0) { return t0 < a.sinks ? t0 : max(t0, sp.ws); };
     auto seen = [&](int t) { return t < sp.len && (t < a.sinks || t >= sp.ws); };
-    auto page_of = [&](int t) { return a.page_shift >= 0 ? t >> a.page_shift : t / a.page_size; };
+    auto page_of = [&](int t) { return (int)((uint64_t)(uint32_t)t * a.page_magic >> a.page_shift); };
 
     uint32_t bad = 0;  // a page id outside the pool was met: the outputs are NaN
 
-    // Where the tile's rows are.  TILED: the page ids of the two sub-tiles and
-    // the slots that they begin at (a sub-tile with no token that is seen
-    // takes the other's place: its page may be gone).  Both are known one
-    // tile before its loads are issued.
-    struct At { int page[2], slot[2]; };
-    auto locate = [&](int v) __attribute__((always_inline)) {
-        At at;
-        const int t0 = tile_t0(v);
-        const int ts = seen_in(t0) & ~15;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            int t = t0 + 16 * u;
-            if (!(t < sp.len && (t < a.sinks || t + 16 > sp.ws))) t = ts;
-            const int p = page_of(t);
-            at.slot[u] = t - p * a.page_size;
-            at.page[u] = *(cint_t *)(uintptr_t)(a.table + seq * a.ld_table + p);
-        }
-        return at;
-    };
     auto checked = [&](int page) __attribute__((always_inline)) {
         const bool out = (unsigned)page >= (unsigned)a.n_pages;
         bad |= out ? 1u : 0u;
         return out ? 0 : page;
     };
 
-    struct Kreg { u4_t w[2][KP]; float sc[2][4]; } kr;
+    // Where the tile's rows are, known one tile before its loads are issued.
+    // TILED: the page ids of the two sub-tiles and the slots that they begin
+    // at (a sub-tile with no token that is seen takes the other's place: its
+    // page may be gone).  Otherwise page and slot of the lane's token (of one
+    // that is seen, if it is not).
+    struct At { int page[TILED ? 2 : 1], slot[TILED ? 2 : 1]; };
+    auto locate = [&](int v) __attribute__((always_inline)) {
+        At at;
+        const int t0 = tile_t0(v);
+        if constexpr (TILED) {
+            const int ts = seen_in(t0) & ~15;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                int t = t0 + 16 * u;
+                if (!(t < sp.len && (t < a.sinks || t + 16 > sp.ws))) t = ts;
+                const int p = page_of(t);
+                at.slot[u] = t - p * a.page_size;
+                at.page[u] = *(cint_t *)(uintptr_t)(a.table + seq * a.ld_table + p);
+            }
+        } else {
+            int t = t0 + (lane & 31);
+            if (!seen(t)) t = seen_in(t0);
+            const int p = page_of(t);
+            at.slot[0] = t - p * a.page_size;
+            at.page[0] = a.table[seq * a.ld_table + p];
+        }
+        return at;
+    };
+
+    // sc: scales of tokens 4g + i and 16 + 4g + i, as the scores have them
+    // (without TILED sc[0]: of the lane's token)
+    struct Kreg { u4_t w[2][KP]; float sc[8]; } kr;
     struct Vreg { Bytes<VB> w[8]; float sc[8]; } vr;
 
-    // (sc of K: tokens 4g + i of the sub-tile, as the scores have them)
     auto load_k_row = [&](const uint8_t *row, u4_t (&w)[KP]) __attribute__((always_inline)) {
 #pragma unroll
         for (int p = 0; p < KP; ++p) {
@@ -258,63 +270,58 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
             __builtin_memcpy(&w[p], row + 64 * p + 16 * g, 16);
         }
     };
-    // the four rows of lane group g in sub-tile u, for the lane's own lookups
-    auto own_row = [&](int v, int t, int64_t &row, int64_t &sc) __attribute__((always_inline)) {
-        const int t0 = tile_t0(v);
-        if (!seen(t)) t = seen_in(t0);
-        const int p = page_of(t);
-        const int page = checked(a.table[seq * a.ld_table + p]);
-        const int slot = t - p * a.page_size;
-        row = page * a.page_stride + kvh * a.head_stride + slot * a.slot_stride;
-        sc = page * a.sc_page + kvh * a.sc_head + slot * a.sc_slot;
+    auto row_of = [&](int page, int slot) __attribute__((always_inline)) {
+        return page * a.page_stride + kvh * a.head_stride + slot * a.slot_stride;
     };
-    auto load_k = [&](int v, const At &at) __attribute__((always_inline)) {
+    auto scale_of = [&](int page, int slot) __attribute__((always_inline)) {
+        return page * a.sc_page + kvh * a.sc_head + slot * a.sc_slot;
+    };
+    auto from_lane = [&](int64_t x, int src) __attribute__((always_inline)) {
+        const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)x, src), hi = (uint32_t)__shfl((int)(uint32_t)(x >> 32), src);
+        return (int64_t)((uint64_t)hi << 32 | lo);
+    };
+    auto load_k = [&](const At &at) __attribute__((always_inline)) {
+        if constexpr (TILED) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            if constexpr (TILED) {
+            for (int u = 0; u < 2; ++u) {
                 const int page = checked(at.page[u]);
-                const uint8_t *base = a.k + page * a.page_stride + kvh * a.head_stride + at.slot[u] * a.slot_stride;
-                load_k_row(base + (uint32_t)(j * (int)a.slot_stride), kr.w[u]);
-                if constexpr (I8) {
-                    const float *sb = a.ks + page * a.sc_page + kvh * a.sc_head + at.slot[u];
-                    __builtin_memcpy(kr.sc[u], sb + 4 * g, 16);
-                }
-            } else {
-                int64_t row, sc;
-                own_row(v, tile_t0(v) + 16 * u + j, row, sc);
-                load_k_row(a.k + row, kr.w[u]);
-                if constexpr (I8) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        own_row(v, tile_t0(v) + 16 * u + 4 * g + i, row, sc);
-                        kr.sc[u][i] = a.ks[sc];
-                    }
-                }
+                load_k_row(a.k + row_of(page, at.slot[u]) + (uint32_t)(j * (int)a.slot_stride), kr.w[u]);
+                if constexpr (I8) __builtin_memcpy(&kr.sc[4 * u], a.ks + scale_of(page, at.slot[u]) + 4 * g, 16);
             }
+        } else {
+            const int page = checked(at.page[0]);
+            const int64_t row = row_of(page, at.slot[0]);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) load_k_row(a.k + from_lane(row, 16 * u + j), kr.w[u]);
+            if constexpr (I8) kr.sc[0] = a.ks[scale_of(page, at.slot[0])];
         }
     };
-    auto load_v = [&](int v, const At &at) __attribute__((always_inline)) {
+    auto load_v = [&](const At &at) __attribute__((always_inline)) {
+        if constexpr (TILED) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            if constexpr (TILED) {
+            for (int u = 0; u < 2; ++u) {
                 const int page = checked(at.page[u]);
-                const uint8_t *base = a.v + page * a.page_stride + kvh * a.head_stride + at.slot[u] * a.slot_stride;
+                const uint8_t *base = a.v + row_of(page, at.slot[u]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     vr.w[4 * u + i] = load_bytes<VB>(base + (uint32_t)((4 * g + i) * (int)a.slot_stride + j * VB));
-                if constexpr (I8) {
-                    const float *sb = a.vs + page * a.sc_page + kvh * a.sc_head + at.slot[u];
-                    __builtin_memcpy(&vr.sc[4 * u], sb + 4 * g, 16);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    int64_t row, sc;
-                    own_row(v, tile_t0(v) + 16 * u + 4 * g + i, row, sc);
-                    vr.w[4 * u + i] = load_bytes<VB>(a.v + row + j * VB);
-                    if constexpr (I8) vr.sc[4 * u + i] = a.vs[sc];
-                }
+                if constexpr (I8) __builtin_memcpy(&vr.sc[4 * u], a.vs + scale_of(page, at.slot[u]) + 4 * g, 16);
             }
+        } else {
+            const int page = checked(at.page[0]);
+            const int64_t row = row_of(page, at.slot[0]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                vr.w[i] = load_bytes<VB>(a.v + from_lane(row, 16 * (i >> 2) + 4 * g + (i & 3)) + j * VB);
+            if constexpr (I8) vr.sc[0] = a.vs[scale_of(page, at.slot[0])];
+        }
+    };
+    // the scales of a lane's tokens, from the lanes that read them
+    auto spread = [&](float (&sc)[8]) __attribute__((always_inline)) {
+        if constexpr (I8 && !TILED) {
+            const float own = sc[0];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sc[i] = __shfl(own, 16 * (i >> 2) + 4 * g + (i & 3));
         }
     };
 
@@ -325,6 +332,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
 
     float s[8];  // scores of tokens 4g + i (0..3) and 16 + 4g + i (4..7), in log2
     auto scores = [&]() __attribute__((always_inline)) {
+        spread(kr.sc);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             f4_t c = {0.0f, 0.0f, 0.0f, 0.0f}, d = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -343,7 +351,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float x = ldexpf(c[i] + d[i], qexp);
-                if constexpr (I8) x *= kr.sc[u][i];
+                if constexpr (I8) x *= kr.sc[4 * u + i];
                 s[4 * u + i] = x;
             }
         }
@@ -381,6 +389,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
             l += p[i];
         }
         if constexpr (I8) {
+            spread(vr.sc);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 p[i] *= vr.sc[i];
@@ -428,16 +437,16 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
     int v = tbeg + wave;
     if (v < tend) {
         At at = locate(v);
-        load_k(v, at);
-        load_v(v, at);
+        load_k(at);
+        load_v(at);
         at = locate(min(v + kAttnWaves, tend - 1));
         for (; v + kAttnWaves < tend; v += kAttnWaves) {
             const int n = v + kAttnWaves;
             scores();
-            load_k(n, at);
+            load_k(at);
             probabilities(v);
             outputs();
-            load_v(n, at);
+            load_v(at);
             at = locate(min(n + kAttnWaves, tend - 1));
         }
         scores();
@@ -496,13 +505,15 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
 }
 
 // Joins the chunks of one (sequence, head): a workgroup's threads take the
-// partial results D/4 threads at a time.
+// partial results D/4 threads at a time, kAttnJoinUnroll chunks in flight.
+constexpr int kAttnJoinUnroll = 8;
 template <int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
     constexpr int COLS = D / 4;
     constexpr int ROWS = 256 / COLS;   // chunks at a time
+    constexpr int U = kAttnJoinUnroll;
     __shared__ __attribute__((aligned(16))) float so[ROWS][D];
-    __shared__ float sl[ROWS];
+    __shared__ float sl[ROWS], sm[ROWS];
     const int head = blockIdx.x % a.n_heads;
     const int seq = blockIdx.x / a.n_heads;
     const int len_in = a.lens[seq];
@@ -510,31 +521,53 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
     const int n = (sp.tiles + a.chunk_tiles - 1) / a.chunk_tiles;
     if (n <= 1) return;  // written already (whole workgroup, before any barrier)
     const float *part = a.part + (int64_t)(seq * (int64_t)a.n_heads + head) * a.nchunks * attn_part_floats(D);
-    float m = kAttnLow;
-    for (int c = threadIdx.x & 63; c < n; c += 64) m = fmaxf(m, part[c * attn_part_floats(D)]);
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
     const int row = threadIdx.x / COLS, col = threadIdx.x % COLS;
     if (row < ROWS) {
         f4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-        float l = 0.0f;
-        for (int c = row; c < n; c += ROWS) {
-            const float *p = part + c * attn_part_floats(D);
-            const float f = __builtin_amdgcn_exp2f(p[0] - m);
-            l += f * p[1];
-            const f4_t x = *reinterpret_cast<const f4_t *>(p + 4 + 4 * col);
+        float l = 0.0f, m = kAttnLow;
+        for (int c0 = row; c0 < n; c0 += U * ROWS) {
+            float pm[U], pl[U];
+            f4_t x[U];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e] += f * x[e];
+            for (int u = 0; u < U; ++u) {
+                // (past the last chunk: the last one again, with weight 0)
+                const float *p = part + min(c0 + u * ROWS, n - 1) * attn_part_floats(D);
+                __builtin_memcpy(&x[u], p + 4 + 4 * col, 16);
+                pm[u] = p[0];
+                pl[u] = p[1];
+            }
+            float top = m;
+#pragma unroll
+            for (int u = 0; u < U; ++u) top = fmaxf(top, pm[u]);
+            const float f0 = __builtin_amdgcn_exp2f(m - top);
+            l *= f0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] *= f0;
+            m = top;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (c0 + u * ROWS >= n) continue;
+                const float f = __builtin_amdgcn_exp2f(pm[u] - top);
+                l += f * pl[u];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[e] += f * x[u][e];
+            }
         }
         *reinterpret_cast<f4_t *>(&so[row][4 * col]) = acc;
-        if (col == 0) sl[row] = l;
+        if (col == 0) {
+            sl[row] = l;
+            sm[row] = m;
+        }
     }
     __syncthreads();
     for (int d = threadIdx.x; d < D; d += 256) {
+        float m = sm[0];
+        for (int r = 1; r < ROWS; ++r) m = fmaxf(m, sm[r]);
         float acc = 0.0f, l = 0.0f;
         for (int r = 0; r < ROWS; ++r) {
-            acc += so[r][d];
-            l += sl[r];
+            const float f = __builtin_amdgcn_exp2f(sm[r] - m);
+            acc += f * so[r][d];
+            l += f * sl[r];
         }
         const float y = acc / l;
         const int64_t at = seq * a.y_seq + head * a.y_head + d;

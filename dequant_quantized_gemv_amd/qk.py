@@ -401,25 +401,62 @@ def mul_mat(fmt, w, m, k, x, y=None, stream=None):
     return y
 
 
+# The calls below run between the products of a decode step, where the time to
+# make them counts: the checks that a well-formed call passes are a few
+# attribute reads, and what refuses is left to the slower helpers above.
+
+def _stream_of(t, stream):
+    """Handle of the caller's stream, or of the current one on t's device."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return _stream(stream)
+
+
+def _on_device(*ts):
+    """_same_device, over tensors of which some may be None."""
+    d = ts[0].get_device()
+    for t in ts:
+        if t is not None and (d < 0 or t.get_device() != d):
+            _same_device(*[u for u in ts if u is not None])
+
+
+def _rows_check(t, name, dtype, n, length):
+    """_cols_check, quick where t is as it should be."""
+    import torch
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == (n, length) and t.is_contiguous():
+        return
+    _cols_check(t, name, dtype, n, length)
+
+
+def _vec_check(t, name, n):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32:
+        raise TypeError(f"{name} must be a float32 tensor")
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous ({n},) tensor, got {tuple(t.shape)}")
+
+
 def mul_mat_vec_x8q(fmt, w, m, k, xq, y=None, stream=None):
     """As mul_mat_vec_x8, over activations in 8 bits already: xq (n, >= k/32*36)
     uint8, rows of 36-byte blocks as rms_norm(..., out_dtype="x8") gives them."""
     import torch
     _weight_check(fmt, w, m, k)
-    if not isinstance(xq, torch.Tensor) or xq.dtype != torch.uint8:
+    if not isinstance(xq, torch.Tensor) or xq.dtype is not torch.uint8:
         raise TypeError("xq must be a uint8 tensor of 8-bit activation blocks")
     if xq.dim() == 1:
         xq = xq.view(1, -1)
     n = xq.shape[0]
     if not 1 <= n <= 8:
         raise ValueError(f"1..8 activation columns, got {n}")
-    _cols_check(xq, "xq", torch.uint8, n, k // 32 * X8_BLOCK_BYTES)
+    _rows_check(xq, "xq", torch.uint8, n, k // 32 * X8_BLOCK_BYTES)
     if y is None:
-        y = torch.empty((n, m), dtype=torch.float32, device=xq.device)
-    _cols_check(y, "y", torch.float32, n, m)
-    _same_device(w, xq, y)
-    st = qk_mul_mat_vec_x8q(fmt, w.data_ptr(), m, k, xq.data_ptr(), n, xq.stride(0), y.data_ptr(), y.stride(0),
-                            _stream(stream))
+        y = xq.new_empty((n, m), dtype=torch.float32)
+    else:
+        _rows_check(y, "y", torch.float32, n, m)
+    _on_device(w, xq, y)
+    st = load().qk_mul_mat_vec_x8q(_fmt(fmt), w.data_ptr(), m, k, xq.data_ptr(), n, xq.stride(0), y.data_ptr(),
+                                   y.stride(0), _stream_of(xq, stream))
     _check(st, "qk_mul_mat_vec_x8q")
     return y
 
@@ -429,48 +466,55 @@ def _row_stride(t):
     return t.stride(0) if t.shape[0] > 1 else 0
 
 
+_NORM_OUT = {"f32": QK_F32, "f16": QK_F16, "x8": QK_X8}
+
+
 def rms_norm(x, weight=None, eps=1e-5, residual=None, out_dtype="f32", y=None, residual_out=None, stream=None):
     """Root-mean-square norm of the rows of x (n, k), fp32 or fp16, after
     adding `residual` (as x): returns y, or (y, x + residual) with a residual.
     out_dtype "f32", "f16", or "x8" (y uint8 (n, k/32*36), 8-bit activation
     blocks for mul_mat_vec_x8q).  residual_out may be x or residual itself."""
     import torch
-    types = {torch.float32: QK_F32, torch.float16: QK_F16}
-    if not isinstance(x, torch.Tensor) or x.dtype not in types:
+    dtype = x.dtype if isinstance(x, torch.Tensor) else None
+    if dtype is torch.float32:
+        code = QK_F32
+    elif dtype is torch.float16:
+        code = QK_F16
+    else:
         raise TypeError("x must be a float32 or float16 tensor")
     if x.dim() != 2 or x.shape[1] < 1:
         raise ValueError(f"x must have shape (n, k) with k >= 1, got {tuple(x.shape)}")
-    outs = {"f32": (QK_F32, torch.float32), "f16": (QK_F16, torch.float16), "x8": (QK_X8, torch.uint8)}
-    if out_dtype not in outs:
+    ycode = _NORM_OUT.get(out_dtype)
+    if ycode is None:
         raise ValueError(f"out_dtype must be 'f32', 'f16' or 'x8', got {out_dtype!r}")
     n, k = x.shape
-    code, dt = outs[out_dtype]
-    if code == QK_X8 and k % 32 != 0:
-        raise ValueError(f"k must be a multiple of 32 for out_dtype 'x8', got {k}")
-    row = k // 32 * X8_BLOCK_BYTES if code == QK_X8 else k
-    _cols_check(x, "x", x.dtype, n, k)
-    if residual is None and residual_out is not None:
-        raise ValueError("residual_out without residual")
+    if ycode == QK_X8:
+        if k % 32 != 0:
+            raise ValueError(f"k must be a multiple of 32 for out_dtype 'x8', got {k}")
+        ydtype, row = torch.uint8, k // 32 * X8_BLOCK_BYTES
+    else:
+        ydtype, row = torch.float32 if ycode == QK_F32 else torch.float16, k
+    _rows_check(x, "x", dtype, n, k)
     if residual is not None:
-        _cols_check(residual, "residual", x.dtype, n, k)
+        _rows_check(residual, "residual", dtype, n, k)
         if residual_out is None:
-            residual_out = torch.empty((n, k), dtype=x.dtype, device=x.device)
-        _cols_check(residual_out, "residual_out", x.dtype, n, k)
+            residual_out = torch.empty_like(residual)
+        else:
+            _rows_check(residual_out, "residual_out", dtype, n, k)
+    elif residual_out is not None:
+        raise ValueError("residual_out without residual")
     if weight is not None:
-        if not isinstance(weight, torch.Tensor) or weight.dtype != torch.float32:
-            raise TypeError("weight must be a float32 tensor")
-        if weight.dim() != 1 or weight.shape[0] != k or weight.stride(0) != 1:
-            raise ValueError(f"weight must be a contiguous ({k},) tensor, got {tuple(weight.shape)}")
+        _vec_check(weight, "weight", k)
     if y is None:
-        y = torch.empty((n, row), dtype=dt, device=x.device)
-    _cols_check(y, "y", dt, n, row)
-    _same_device(x, y, *[t for t in (residual, residual_out, weight) if t is not None])
-
-    def at(t):
-        return (0, 0) if t is None else (t.data_ptr(), t.stride(0))
-
-    st = qk_rms_norm(types[x.dtype], *at(x), *at(residual), at(weight)[0], float(eps), n, k, *at(residual_out), code,
-                     *at(y), _stream(stream))
+        y = torch.empty_like(x) if ydtype is dtype else x.new_empty((n, row), dtype=ydtype)
+    else:
+        _rows_check(y, "y", ydtype, n, row)
+    _on_device(x, y, residual, residual_out, weight)
+    r, ldr, s, lds = None, 0, None, 0
+    if residual is not None:
+        r, ldr, s, lds = residual.data_ptr(), residual.stride(0), residual_out.data_ptr(), residual_out.stride(0)
+    st = load().qk_rms_norm(code, x.data_ptr(), x.stride(0), r, ldr, weight.data_ptr() if weight is not None else None,
+                            eps, n, k, s, lds, ycode, y.data_ptr(), y.stride(0), _stream_of(x, stream))
     _check(st, "qk_rms_norm")
     return y if residual is None else (y, residual_out)
 
@@ -539,17 +583,17 @@ class KVCache:
 
 def _int32_check(t, name, dim):
     import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32:
         raise TypeError(f"{name} must be an int32 tensor")
-    if t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    if t.dim() != dim or (not t.is_contiguous() and t.shape[-1] > 1 and t.stride(-1) != 1):
         raise ValueError(f"{name} must be {dim}-dimensional with contiguous rows, got {tuple(t.shape)}")
 
 
 def _heads_check(t, name, dtype, n, heads, dim):
     import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
         raise TypeError(f"{name} must be a {dtype} tensor")
-    if tuple(t.shape) != (n, heads, dim) or (n > 0 and t.stride(2) != 1):
+    if t.shape != (n, heads, dim) or (not t.is_contiguous() and t.stride(2) != 1):
         raise ValueError(f"{name} must have shape ({n}, {heads}, {dim}) with contiguous rows, got {tuple(t.shape)}")
 
 
@@ -571,11 +615,11 @@ def kv_store(cache, k, v, table, pos, seq=None, stream=None):
         raise ValueError(f"table has {table.shape[0]} sequences for {n} tokens")
     for t, name in ((k, "k"), (v, "v")):
         _heads_check(t, name, torch.float32, n, cache.n_heads, cache.head_dim)
-    _same_device(cache.k, k, v, table, pos, *([seq] if seq is not None else []))
-    st = qk_kv_store(cache.desc, k.data_ptr(), _row_stride(k), k.stride(1) if cache.n_heads > 1 else 0,
-                     v.data_ptr(), _row_stride(v), v.stride(1) if cache.n_heads > 1 else 0,
-                     n, table.data_ptr(), table.stride(0), table.shape[0], table.shape[1],
-                     seq.data_ptr() if seq is not None else None, pos.data_ptr(), _stream(stream))
+    _on_device(cache.k, k, v, table, pos, seq)
+    st = load().qk_kv_store(cache.desc, k.data_ptr(), _row_stride(k), k.stride(1) if cache.n_heads > 1 else 0,
+                            v.data_ptr(), _row_stride(v), v.stride(1) if cache.n_heads > 1 else 0,
+                            n, table.data_ptr(), table.stride(0), table.shape[0], table.shape[1],
+                            seq.data_ptr() if seq is not None else None, pos.data_ptr(), _stream_of(pos, stream))
     _check(st, "qk_kv_store")
 
 
@@ -597,9 +641,12 @@ def attn_decode(cache, q, table, lens, scale=None, window=0, sinks=0, max_len=No
     the split over the cache; a length above it gives NaN.  Returns y (n_seqs,
     n_q_heads, head_dim), fp32 or (out_dtype "f16") fp16."""
     import torch
-    if out_dtype not in ("f32", "f16"):
+    if out_dtype == "f32":
+        code, dt = QK_F32, torch.float32
+    elif out_dtype == "f16":
+        code, dt = QK_F16, torch.float16
+    else:
         raise ValueError(f"out_dtype must be 'f32' or 'f16', got {out_dtype!r}")
-    code, dt = {"f32": (QK_F32, torch.float32), "f16": (QK_F16, torch.float16)}[out_dtype]
     _int32_check(table, "table", 2)
     _int32_check(lens, "lens", 1)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
@@ -617,28 +664,31 @@ def attn_decode(cache, q, table, lens, scale=None, window=0, sinks=0, max_len=No
     if window < 0 or sinks < 0:
         raise ValueError("window and sinks must not be negative")
     if y is None:
-        y = torch.empty((n, heads, dim), dtype=dt, device=q.device)
-    _heads_check(y, "y", dt, n, heads, dim)
-    need = qk_attn_decode_workspace(cache.desc, n, heads, max_len, window, sinks)
-    handle = _stream(stream)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if handle != torch.cuda.current_stream(q.device).cuda_stream:
-            # not to be given out again before the other stream is done with it
-            workspace.record_stream(torch.cuda.ExternalStream(handle, device=q.device))
-    if workspace is not None:
-        if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-            raise TypeError("workspace must be a contiguous uint8 tensor")
-        if workspace.numel() < need:
-            raise ValueError(f"workspace holds {workspace.numel()} bytes, {need} are needed")
-    _same_device(cache.k, q, table, lens, y, *([workspace] if workspace is not None else []))
-    st = qk_attn_decode(cache.desc, q.data_ptr(), _row_stride(q), q.stride(1) if heads > 1 else 0, n, heads,
-                        table.data_ptr(), table.stride(0), lens.data_ptr(), max_len,
-                        dim ** -0.5 if scale is None else float(scale), window, sinks, code, y.data_ptr(),
-                        _row_stride(y), y.stride(1) if heads > 1 else 0,
-                        workspace.data_ptr() if workspace is not None else None, need, handle)
+        y = q.new_empty((n, heads, dim), dtype=dt)
+    else:
+        _heads_check(y, "y", dt, n, heads, dim)
+    _on_device(cache.k, q, table, lens, y, workspace)
+    handle = _stream_of(q, stream)
+    if workspace is None:
+        need = qk_attn_decode_workspace(cache.desc, n, heads, max_len, window, sinks)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            if stream is not None and handle != _stream_of(q, None):
+                # not to be given out again before the other stream is done with it
+                workspace.record_stream(torch.cuda.ExternalStream(handle, device=q.device))
+    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous uint8 tensor")
+    q_head, y_head = (q.stride(1), y.stride(1)) if heads > 1 else (0, 0)
+    st = load().qk_attn_decode(cache.desc, q.data_ptr(), _row_stride(q), q_head, n, heads, table.data_ptr(),
+                               table.stride(0), lens.data_ptr(), max_len, dim ** -0.5 if scale is None else scale,
+                               window, sinks, code, y.data_ptr(), _row_stride(y), y_head,
+                               workspace.data_ptr() if workspace is not None else None,
+                               workspace.numel() if workspace is not None else 0, handle)
     _check(st, "qk_attn_decode")
     return y
+
+
+_SCORES = {"softmax": QK_SOFTMAX, "sigmoid": QK_SIGMOID}
 
 
 def moe_route(logits, n_used, score="softmax", bias=None, n_groups=1, topk_groups=1, group_top=1, renorm=True,
@@ -650,34 +700,30 @@ def moe_route(logits, n_used, score="softmax", bias=None, n_groups=1, topk_group
     topk_groups best groups of neighbouring experts take part, by the sum of
     their group_top (1 or 2) largest values."""
     import torch
-    scores = {"softmax": QK_SOFTMAX, "sigmoid": QK_SIGMOID}
-    if score not in scores:
+    code = _SCORES.get(score)
+    if code is None:
         raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
-    if not isinstance(logits, torch.Tensor) or logits.dtype != torch.float32:
+    if not isinstance(logits, torch.Tensor) or logits.dtype is not torch.float32:
         raise TypeError("logits must be a float32 tensor")
-    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+    if logits.dim() != 2 or (not logits.is_contiguous() and logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError(f"logits must be (n_tokens, n_experts) with contiguous rows, got {tuple(logits.shape)}")
     n, experts = logits.shape
     if bias is not None:
-        if not isinstance(bias, torch.Tensor) or bias.dtype != torch.float32:
-            raise TypeError("bias must be a float32 tensor")
-        if bias.dim() != 1 or bias.shape[0] != experts or bias.stride(0) != 1:
-            raise ValueError(f"bias must be a contiguous ({experts},) tensor, got {tuple(bias.shape)}")
+        _vec_check(bias, "bias", experts)
     if not 1 <= n_used <= 64:
         raise ValueError(f"n_used must be 1..64, got {n_used}")
     if ids is None:
-        ids = torch.empty((n, n_used), dtype=torch.int32, device=logits.device)
+        ids = logits.new_empty((n, n_used), dtype=torch.int32)
+    else:
+        _rows_check(ids, "ids", torch.int32, n, n_used)
     if weights is None:
-        weights = torch.empty((n, n_used), dtype=torch.float32, device=logits.device)
-    for t, name, dt in ((ids, "ids", torch.int32), (weights, "weights", torch.float32)):
-        if not isinstance(t, torch.Tensor) or t.dtype != dt:
-            raise TypeError(f"{name} must be a {dt} tensor")
-        if tuple(t.shape) != (n, n_used) or (n_used > 1 and t.stride(1) != 1):
-            raise ValueError(f"{name} must have shape ({n}, {n_used}) with contiguous rows, got {tuple(t.shape)}")
-    _same_device(logits, ids, weights, *([bias] if bias is not None else []))
-    st = qk_moe_route(logits.data_ptr(), logits.stride(0), n, experts, n_used, scores[score],
-                      bias.data_ptr() if bias is not None else None, n_groups, topk_groups, group_top, int(renorm),
-                      float(scale), ids.data_ptr(), ids.stride(0), weights.data_ptr(), weights.stride(0),
-                      _stream(stream))
+        weights = logits.new_empty((n, n_used))
+    else:
+        _rows_check(weights, "weights", torch.float32, n, n_used)
+    _on_device(logits, ids, weights, bias)
+    st = load().qk_moe_route(logits.data_ptr(), logits.stride(0), n, experts, n_used, code,
+                             bias.data_ptr() if bias is not None else None, n_groups, topk_groups, group_top,
+                             1 if renorm else 0, scale, ids.data_ptr(), ids.stride(0), weights.data_ptr(),
+                             weights.stride(0), _stream_of(logits, stream))
     _check(st, "qk_moe_route")
     return ids, weights
