@@ -143,19 +143,53 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, j = lane & 15;
+    // Chunks outermost: workgroups go round the XCDs in turn, so with chunks
+    // innermost the chunks that only long sequences have would meet on the
+    // same XCDs; and a sequence's first chunks, which are whole, start first.
     int b = blockIdx.x;
-    const int chunk = b % a.nchunks;
-    b /= a.nchunks;
+    const int rows = gridDim.x / a.nchunks;
+    const int chunk = b / rows;
+    b -= chunk * rows;
     const int ht = b % a.head_tiles;
     b /= a.head_tiles;
     const int kvh = b % a.n_kv;
     const int seq = b / a.n_kv;
 
-    const int len_in = *(cint_t *)(uintptr_t)(a.lens + seq);
-    const bool too_long = len_in > a.max_len;
-    const AttnSpan sp = attn_span(len_in < 0 ? 0 : too_long ? 0 : len_in, a.window, a.sinks);
     const int head0 = kvh * a.group + ht * kAttnHeads;
     const int nh = min(kAttnHeads, a.group - ht * kAttnHeads);
+    auto page_of = [&](int t) { return (int)((uint64_t)(uint32_t)t * a.page_magic >> a.page_shift); };
+
+    // What waits for no other load is asked for first: the length, the first
+    // tile's pages (where there is no window they follow from the chunk), q.
+    const int len_in = *(cint_t *)(uintptr_t)(a.lens + seq);
+    const int tbeg = chunk * a.chunk_tiles;
+    int first_page[2] = {0, 0};
+    if (TILED && a.window == 0) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int t = min(kAttnTile * (tbeg + wave) + 16 * u, a.max_len - 1);
+            first_page[u] = *(cint_t *)(uintptr_t)(a.table + seq * a.ld_table + page_of(t));
+        }
+    }
+    // lane (g, j) holds head j, the dims that its K pieces hold
+    auto dim_of = [&](int s) {  // first of step s's eight dims in this lane
+        if constexpr (I8) {
+            if (STEPS % 2 == 1 && s == STEPS - 1) return 32 * s + 8 * g;
+            return 64 * (s >> 1) + 16 * g + 8 * (s & 1);
+        } else {
+            return 32 * s + 8 * g;
+        }
+    };
+    float qv[STEPS][8];
+    {
+        const float *q = a.q + seq * a.q_seq + (int64_t)(head0 + min(j, nh - 1)) * a.q_head;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) __builtin_memcpy(qv[s], q + dim_of(s), 32);
+    }
+    asm volatile("" ::: "memory");  // (keeps the loads of q ahead of those of K and V, which it does not wait for)
+
+    const bool too_long = len_in > a.max_len;
+    const AttnSpan sp = attn_span(len_in < 0 ? 0 : too_long ? 0 : len_in, a.window, a.sinks);
     if (sp.tiles == 0) {
         // no token to see: zeros (NaN where the length is past max_len)
         if (chunk == 0) {
@@ -168,33 +202,20 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
         }
         return;
     }
-    const int tbeg = chunk * a.chunk_tiles;
     const int tend = min(tbeg + a.chunk_tiles, sp.tiles);
     if (tbeg >= tend) return;  // (whole workgroup, before any barrier)
 
-    // q: lane (g, j) holds head j, the dims that its K pieces hold
-    auto dim_of = [&](int s) {  // first of step s's eight dims in this lane
-        if constexpr (I8) {
-            if (STEPS % 2 == 1 && s == STEPS - 1) return 32 * s + 8 * g;
-            return 64 * (s >> 1) + 16 * g + 8 * (s & 1);
-        } else {
-            return 32 * s + 8 * g;
-        }
-    };
     h8_t qh[STEPS], ql[STEPS];
     int qexp = 0;
-    {
-        const float *q = a.q + seq * a.q_seq + (int64_t)(head0 + min(j, nh - 1)) * a.q_head;
-        float qv[STEPS][8], top = 0.0f;
+    auto split_q = [&]() __attribute__((always_inline)) {
+        float top = 0.0f;
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            __builtin_memcpy(qv[s], q + dim_of(s), 32);
+        for (int s = 0; s < STEPS; ++s)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 qv[s][i] *= a.qscale;
                 top = fmaxf(top, fabsf(qv[s][i]));
             }
-        }
         top = quad_rows_max(top);
         int ex = 14;
         if (top > 0.0f && top <= 3.402823466e38f) (void)frexpf(top, &ex);
@@ -206,13 +227,12 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
             split8(qv[s], qh[s], ql[s]);
         }
         if constexpr (I8) qexp += 9;  // codes are held times 2^-9
-    }
+    };
 
     auto tile_t0 = [&](int v) { return v < sp.ns ? kAttnTile * v : sp.start + kAttnTile * (v - sp.ns); };
     // a token that is seen in the tile at t0
     auto seen_in = [&](int t0) { return t0 < a.sinks ? t0 : max(t0, sp.ws); };
     auto seen = [&](int t) { return t < sp.len && (t < a.sinks || t >= sp.ws); };
-    auto page_of = [&](int t) { return (int)((uint64_t)(uint32_t)t * a.page_magic >> a.page_shift); };
 
     uint32_t bad = 0;  // a page id outside the pool was met: the outputs are NaN
 
@@ -436,10 +456,23 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
     // scores are done, its V registers as soon as its outputs are.
     int v = tbeg + wave;
     if (v < tend) {
-        At at = locate(v);
+        At at;
+        if (TILED && a.window == 0) {
+            const bool both = kAttnTile * v + 16 < sp.len;
+#pragma unroll
+            for (int u = 0; u < (TILED ? 2 : 1); ++u) {
+                const int t = kAttnTile * v + (both ? 16 * u : 0);
+                at.page[u] = both ? first_page[u] : first_page[0];
+                at.slot[u] = t - page_of(t) * a.page_size;
+            }
+        } else {
+            at = locate(v);
+        }
         load_k(at);
         load_v(at);
         at = locate(min(v + kAttnWaves, tend - 1));
+        asm volatile("" ::: "memory");
+        split_q();
         for (; v + kAttnWaves < tend; v += kAttnWaves) {
             const int n = v + kAttnWaves;
             scores();
