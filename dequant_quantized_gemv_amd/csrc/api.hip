@@ -122,7 +122,7 @@ Ranges cache_ranges(const qk_kv_cache &c) {
 }
 
 #ifndef QK_ATTN_WG_PER_CU
-#define QK_ATTN_WG_PER_CU 4
+#define QK_ATTN_WG_PER_CU 2
 #endif
 // Sizes and the split of a decode attention over the cache's length: the
 // tokens of a sequence go to workgroups in chunks of `chunk_tiles` 32-token
@@ -443,7 +443,7 @@ int qk_kv_store(const qk_kv_cache *cache, const float *k, int64_t k_tok, int64_t
     const qk::StoreArgs a{static_cast<uint8_t *>(c.k), static_cast<uint8_t *>(c.v), c.k_scale, c.v_scale, k, v,
                           table, seq, pos, c.page_stride, c.head_stride, c.slot_stride,
                           c.scale_page_stride, c.scale_head_stride, c.scale_slot_stride,
-                          k_tok, k_head, v_tok, v_head, ld_table, n_tokens * c.n_heads,
+                          k_tok, k_head, v_tok, v_head, ld_table, n_tokens,
                           (int)n_seqs, (int)max_pages, (int)c.n_pages, (int)c.page_size, (int)c.n_heads, (int)c.head_dim};
     return qk::launch_kv_store(a, c.type == QK_KV_I8, static_cast<hipStream_t>(stream));
 }

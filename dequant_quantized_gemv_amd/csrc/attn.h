@@ -64,7 +64,7 @@ struct StoreArgs {
     int64_t sc_page, sc_head, sc_slot;
     int64_t k_tok, k_head, v_tok, v_head;
     int64_t ld_table;
-    int64_t rows;                  // tokens * heads
+    int64_t tokens;
     int n_seqs, max_pages, n_pages, page_size, n_kv, head_dim;
 };
 

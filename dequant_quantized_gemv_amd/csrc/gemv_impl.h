@@ -1157,7 +1157,7 @@ constexpr int kGvMaxWgPerCu = QK_GEMV_WG_PER_CU;
 constexpr int kGvX8MaxWgPerCu = QK_GEMV_X8_WG_PER_CU;
 // Stored blocks cost a workgroup a copy and no quantization.
 #ifndef QK_GEMV_X8Q_WG_PER_CU
-#define QK_GEMV_X8Q_WG_PER_CU 4
+#define QK_GEMV_X8Q_WG_PER_CU 2
 #endif
 constexpr int kGvX8StoredMaxWgPerCu = QK_GEMV_X8Q_WG_PER_CU;
 
