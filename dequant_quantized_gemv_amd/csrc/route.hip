@@ -54,6 +54,19 @@ __device__ __forceinline__ float value_of(uint32_t k) {
     return __builtin_bit_cast(float, k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
+// What a DPP move brings from another lane.
+template <int CTRL>
+__device__ __forceinline__ uint32_t from_dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+
+// Key of a group's score: of its largest value, or of the sum of its two.
+__device__ __forceinline__ uint32_t group_key(uint32_t k0, uint32_t k1, bool two) {
+    if (!two) return k0;
+    const float nan = __builtin_nanf("");
+    return key_of((k0 == 1u ? nan : value_of(k0)) + (k1 == 1u ? nan : value_of(k1)));
+}
+
 template <int V>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs a) {
     const int lane = threadIdx.x & 63;
@@ -102,68 +115,88 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
 
     if (a.kept < a.groups) {
         const int size = a.experts / a.groups;
-        uint32_t mine = 0;  // lane q: key of group q's score
-        for (int q = 0; q < a.groups; ++q) {
-            // the group's largest value, and its next where two are summed
+        const int lanes = size / V;
+        if (size % V == 0 && (lanes & (lanes - 1)) == 0) {
+            // a group is a segment of 1, 2, 4 .. lanes: all groups' two largest at once
             uint32_t b0 = 0, b1 = 0;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const uint32_t k = (unsigned)(e0 + i - q * size) < (unsigned)size ? key[i] : 0u;
-                if (k > b0) {
-                    b1 = b0;
-                    b0 = k;
-                } else if (k > b1) {
-                    b1 = k;
-                }
+                b1 = max(b1, min(b0, key[i]));
+                b0 = max(b0, key[i]);
             }
-            const uint32_t m0 = wave_max(b0);
-            float score = m0 == 1u ? __builtin_nanf("") : value_of(m0);
-            if (a.best == 2 && size > 1) {
-                const uint64_t has = __ballot(b0 == m0);
-                const int first = __builtin_ctzll(has);
-                const uint32_t m1 = wave_max(lane == first ? b1 : b0);
-                score += m1 == 1u ? __builtin_nanf("") : value_of(m1);
+            auto join = [&](uint32_t o0, uint32_t o1) {
+                b1 = max(max(b1, o1), min(b0, o0));
+                b0 = max(b0, o0);
+            };
+            if (lanes > 1) join(from_dpp<0xB1>(b0), from_dpp<0xB1>(b1));
+            if (lanes > 2) join(from_dpp<0x4E>(b0), from_dpp<0x4E>(b1));
+            if (lanes > 4) join(from_dpp<0x141>(b0), from_dpp<0x141>(b1));
+            if (lanes > 8) join(from_dpp<0x140>(b0), from_dpp<0x140>(b1));
+            if (lanes > 16) join((uint32_t)__shfl_xor((int)b0, 16), (uint32_t)__shfl_xor((int)b1, 16));
+            const uint32_t mine = group_key(b0, b1, a.best == 2 && size > 1);
+            // its rank among the groups, of equal ones the first ahead
+            const int group = lane / lanes;
+            int rank = 0;
+            for (int q = 0; q < a.groups; ++q) {
+                const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)mine, q * lanes);
+                rank += other > mine || (other == mine && q < group) ? 1 : 0;
             }
-            const uint32_t k = key_of(score);
-            if (lane == q) mine = k;
-        }
-        uint64_t keep = 0;
-        for (int q = 0; q < a.kept; ++q) {
-            const uint32_t m = wave_max(mine);
-            const int first = __builtin_ctzll(__ballot(mine == m));
-            keep |= 1ull << first;
-            if (lane == first) mine = 0;
-        }
+            if (rank >= a.kept) {
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (e0 + i < a.experts && !(keep >> ((e0 + i) / size) & 1)) key[i] = 0u;
+                for (int i = 0; i < V; ++i) key[i] = 0u;
+            }
+        } else {
+            uint32_t mine = 0;  // lane q: key of group q's score
+            for (int q = 0; q < a.groups; ++q) {
+                uint32_t b0 = 0, b1 = 0;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const uint32_t k = (unsigned)(e0 + i - q * size) < (unsigned)size ? key[i] : 0u;
+                    b1 = max(b1, min(b0, k));
+                    b0 = max(b0, k);
+                }
+                const uint32_t m0 = wave_max(b0);
+                const int first = __builtin_ctzll(__ballot(b0 == m0));
+                const uint32_t m1 = wave_max(lane == first ? b1 : b0);
+                const uint32_t k = group_key(m0, m1, a.best == 2 && size > 1);
+                if (lane == q) mine = k;
+            }
+            uint64_t keep = 0;
+            for (int q = 0; q < a.kept; ++q) {
+                const uint32_t m = wave_max(mine);
+                const int first = __builtin_ctzll(__ballot(mine == m));
+                keep |= 1ull << first;
+                if (lane == first) mine = 0;
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (e0 + i < a.experts && !(keep >> ((e0 + i) / size) & 1)) key[i] = 0u;
+        }
     }
 
     // the best `used`, one after another; lane s keeps choice s
     int my_id = 0;
-    float my_w = 0.0f;
     for (int s = 0; s < a.used; ++s) {
         uint32_t b = key[0];
         int bi = 0;
-        float bp = p[0];
 #pragma unroll
         for (int i = 1; i < V; ++i)
             if (key[i] > b) {
                 b = key[i];
                 bi = i;
-                bp = p[i];
             }
         const uint32_t m = wave_max(b);
         const int first = __builtin_ctzll(__ballot(b == m));
-        const int id = first * V + __builtin_amdgcn_readlane(bi, first);
-        const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, bp), first));
-        if (lane == s) {
-            my_id = id;
-            my_w = w;
-        }
+        const int slot = __builtin_amdgcn_readlane(bi, first);
+        my_id = lane == s ? first * V + slot : my_id;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (e0 + i == id) key[i] = 0u;
+        for (int i = 0; i < V; ++i) key[i] = lane == first && i == slot ? 0u : key[i];
+    }
+    float my_w = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float w = __shfl(p[i], my_id / V);
+        my_w = my_id % V == i ? w : my_w;
     }
     if (a.renorm) {
         const float sum = wave_sum(lane < a.used ? my_w : 0.0f);
