@@ -20,8 +20,8 @@ BENCH_SOURCE = "bench_support.hip"
 BENCH_LIB = os.path.join(PKG, "libqk_bench.so")
 SOURCES = ["api.hip", "dequant.hip", "gemv.hip", "gemv_n1.hip", "gemv_n2.hip", "gemv_n34.hip",
            "gemv_n56.hip", "gemv_n78.hip", "gemv_id.hip", "gemv_x8_n1.hip", "gemv_x8_n24.hip",
-           "gemv_x8_n58.hip", "gemv_x8q_n1.hip", "gemv_x8q_n24.hip", "gemv_x8q_n58.hip", "gemm.hip",
-           "norm.hip", "kv_store.hip", "attn_f16.hip", "attn_i8.hip", "route.hip"]
+           "gemv_x8_n58.hip", "gemv_x8q_n1.hip", "gemv_x8q_n23.hip", "gemv_x8q_mfma.hip",
+           "gemm.hip", "norm.hip", "kv_store.hip", "attn_f16.hip", "attn_i8.hip", "route.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

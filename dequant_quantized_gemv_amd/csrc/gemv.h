@@ -70,6 +70,10 @@ constexpr int kX8BlockBytes = 36;
 template <int NC, int X8>
 int gemv_table_x8(int fmt, GemvArgs &a, bool fast, hipStream_t stream);
 
+// One problem with stored 8-bit activations (1..8 columns) on the matrix cores
+// (gemv_x8q_mfma.hip); weights at any 2-byte boundary, nb >= 1.
+int gemv_x8q_mfma(int fmt, const GemvItem &it, int n, hipStream_t stream);
+
 // Launch expert-indexed problems (same `fast` condition, for every expert and
 // slot).
 int gemv_expert(int fmt, const GemvExpert &e, bool fast, hipStream_t stream);

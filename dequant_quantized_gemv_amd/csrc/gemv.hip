@@ -119,16 +119,34 @@ static int launch_x8(int fmt, const void *w, int64_t m, int64_t k, const float *
     d.nb = (int)(k / kBlockElems);
     a.count = 1;
     const bool fast = ((uintptr_t)d.w % 4) == 0 && (d.nb % 2) == 0;
-    switch (n) {
-    case 1: return gemv_table_x8<1, X8>(fmt, a, fast, stream);
-    case 2: return gemv_table_x8<2, X8>(fmt, a, fast, stream);
-    case 3: return gemv_table_x8<3, X8>(fmt, a, fast, stream);
-    case 4: return gemv_table_x8<4, X8>(fmt, a, fast, stream);
-    case 5: return gemv_table_x8<5, X8>(fmt, a, fast, stream);
-    case 6: return gemv_table_x8<6, X8>(fmt, a, fast, stream);
-    case 7: return gemv_table_x8<7, X8>(fmt, a, fast, stream);
-    case 8: return gemv_table_x8<8, X8>(fmt, a, fast, stream);
-    default: return QK_ERR_INVALID_ARG;
+    if constexpr (X8 == kX8Stored) {
+        // The matrix cores cost the same for 1..8 columns, the vector ALU a
+        // column at a time (us, matrix cores against vector ALU): 4096 x 4096
+        // Q4_0 at 2 / 3 / 4 / 8 columns 5.2 / 5.2 / 5.2 / 5.4 against 5.6 / 5.9 / 6.2
+        // / 8.7, Q8_0 6.5 / 6.6 / 6.6 / 6.9 against 6.4 / 6.7 / 7.4 / 9.9; 11008 x 4096
+        // Q4_0 at 2 / 3 / 8 9.5 / 9.4 / 9.6 against 8.9 / 9.7 / 16.5; with too few
+        // rows for the CUs, 1376 x 4096 Q4_0 at 2 / 3 / 4 4.5 / 4.5 / 4.5 against 3.8
+        // / 4.1 / 5.1.  Rows of up to 64 blocks leave the vector kernel's lanes
+        // idle: 4096 x 1376 Q4_0 at 2 3.8 against 5.3.
+        const bool mfma = n >= 4 || (n >= 2 && d.nb <= 64) || (n == 3 && fast && d.m >= 4096);
+        if (mfma) return gemv_x8q_mfma(fmt, d, (int)n, stream);
+        switch (n) {
+        case 1: return gemv_table_x8<1, X8>(fmt, a, fast, stream);
+        case 2: return gemv_table_x8<2, X8>(fmt, a, fast, stream);
+        default: return gemv_table_x8<3, X8>(fmt, a, fast, stream);
+        }
+    } else {
+        switch (n) {
+        case 1: return gemv_table_x8<1, X8>(fmt, a, fast, stream);
+        case 2: return gemv_table_x8<2, X8>(fmt, a, fast, stream);
+        case 3: return gemv_table_x8<3, X8>(fmt, a, fast, stream);
+        case 4: return gemv_table_x8<4, X8>(fmt, a, fast, stream);
+        case 5: return gemv_table_x8<5, X8>(fmt, a, fast, stream);
+        case 6: return gemv_table_x8<6, X8>(fmt, a, fast, stream);
+        case 7: return gemv_table_x8<7, X8>(fmt, a, fast, stream);
+        case 8: return gemv_table_x8<8, X8>(fmt, a, fast, stream);
+        default: return QK_ERR_INVALID_ARG;
+        }
     }
 }
 

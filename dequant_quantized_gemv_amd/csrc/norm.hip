@@ -59,7 +59,8 @@ __device__ __forceinline__ void store4(T *p, int c, int k, const f4_t &v) {
         t4 t;
 #pragma unroll
         for (int i = 0; i < 4; ++i) t[i] = (T)v[i];
-        put<STREAM>(reinterpret_cast<t4 *>(p + c), t);
+        if constexpr (STREAM) __builtin_nontemporal_store(t, reinterpret_cast<t4 *>(p + c));
+        else *reinterpret_cast<t4 *>(p + c) = t;
     } else {
 #pragma unroll
         for (int i = 0; i < 3; ++i)

@@ -186,10 +186,12 @@ int qk_mul_mat_vec_x8(int fmt, const void *w, int64_t m, int64_t k,
 /*
  * qk_mul_mat_vec_x8q - qk_mul_mat_vec_x8 over activations that are in 8 bits
  * already: x is n columns of k/32 QK_X8 blocks (fp32 scale, 32 int8 codes),
- * as qk_rms_norm writes them.  With the blocks that qk_mul_mat_vec_x8 makes
- * of the same activations the outputs are the same, bit for bit; several
- * products of one vector then share one quantization.  Any scale and codes
- * -128..127 are taken.
+ * as qk_rms_norm writes them; several products of one vector then share one
+ * quantization.  Any scale and codes -128..127 are taken.  With the blocks that
+ * qk_mul_mat_vec_x8 makes of the same activations the outputs of one column
+ * are the same, bit for bit; more columns may run on the matrix cores (exact
+ * integer products, fp32 sums over the blocks in another order), and the two
+ * then agree within the error bound.
  *
  *   xq         QK_X8 blocks, 4-byte aligned; column j starts at byte j*ldx
  *   ldx        bytes, a multiple of 4, >= k/32*36 (ignored if n == 1)
