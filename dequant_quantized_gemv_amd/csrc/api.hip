@@ -121,14 +121,17 @@ Ranges cache_ranges(const qk_kv_cache &c) {
     return out;
 }
 
-#ifndef QK_ATTN_WG_PER_CU
-#define QK_ATTN_WG_PER_CU 2
-#endif
 // Sizes and the split of a decode attention over the cache's length: the
 // tokens of a sequence go to workgroups in chunks of `chunk_tiles` 32-token
 // tiles.  The lengths are on the device, so the chunk follows from max_len:
-// enough chunks to give every CU a few workgroups, and at least one tile for
-// each wave of a workgroup.
+// enough chunks to give every CU two workgroups (one where head_dim leaves room
+// for one wave per SIMD), and at least one tile for each wave of a workgroup.
+// A workgroup's first rows wait for its length, page ids and keys one after
+// another, so more and shorter chunks cost more than their balance gives:
+// 131072 tokens of 8 x 128 in fp16 at 2 / 3 / 4 / 8 / 16 workgroups per CU 100.7 /
+// 101.8 / 105 / 110 / 121 us; 64 sequences of 2048 tokens in 8 bits 57 / - / 63 / 67 /
+// -, of 64..4096 tokens 75 / 74 / 74 / 73 / 74; head_dim 256, 131072 tokens of 2
+// heads at 1 / 2 61 / 72.
 int attn_plan(const qk_kv_cache &c, int64_t n_seqs, int64_t n_q_heads, int64_t max_len, int64_t window,
               int64_t sinks, qk::AttnArgs &a) {
     if (n_seqs < 0 || n_seqs > kMaxDim || n_q_heads < 1 || n_q_heads % c.n_heads != 0 || n_q_heads > (1 << 20) ||
@@ -157,7 +160,7 @@ int attn_plan(const qk_kv_cache &c, int64_t n_seqs, int64_t n_q_heads, int64_t m
         tiles = std::min<int64_t>(tiles, (a.sinks + qk::kAttnTile - 1) / qk::kAttnTile +
                                              (a.window + qk::kAttnTile - 1) / qk::kAttnTile + 1);
     const int64_t rows = n_seqs * a.n_kv * a.head_tiles;
-    const int64_t target = QK_ATTN_WG_PER_CU * (int64_t)qk::device_cus();
+    const int64_t target = (c.head_dim <= 128 ? 2 : 1) * (int64_t)qk::device_cus();
     int64_t chunk = (tiles * rows + target - 1) / target;
     chunk = std::max<int64_t>(qk::kAttnWaves, (chunk + qk::kAttnWaves - 1) / qk::kAttnWaves * qk::kAttnWaves);
     a.chunk_tiles = (int)std::min<int64_t>(chunk, tiles);
