@@ -422,11 +422,12 @@ def _on_device(*ts):
 
 
 def _rows_check(t, name, dtype, n, length):
-    """_cols_check, quick where t is as it should be."""
+    """_cols_check, quick where t is as it should be; the stride of its rows."""
     import torch
     if type(t) is torch.Tensor and t.dtype is dtype and t.shape == (n, length) and t.is_contiguous():
-        return
+        return length
     _cols_check(t, name, dtype, n, length)
+    return t.stride(0)
 
 
 def _vec_check(t, name, n):
@@ -449,14 +450,14 @@ def mul_mat_vec_x8q(fmt, w, m, k, xq, y=None, stream=None):
     n = xq.shape[0]
     if not 1 <= n <= 8:
         raise ValueError(f"1..8 activation columns, got {n}")
-    _rows_check(xq, "xq", torch.uint8, n, k // 32 * X8_BLOCK_BYTES)
+    ldx = _rows_check(xq, "xq", torch.uint8, n, k // 32 * X8_BLOCK_BYTES)
     if y is None:
-        y = xq.new_empty((n, m), dtype=torch.float32)
+        y, ldy = xq.new_empty((n, m), dtype=torch.float32), m
     else:
-        _rows_check(y, "y", torch.float32, n, m)
+        ldy = _rows_check(y, "y", torch.float32, n, m)
     _on_device(w, xq, y)
-    st = load().qk_mul_mat_vec_x8q(_fmt(fmt), w.data_ptr(), m, k, xq.data_ptr(), n, xq.stride(0), y.data_ptr(),
-                                   y.stride(0), _stream_of(xq, stream))
+    st = load().qk_mul_mat_vec_x8q(_fmt(fmt), w.data_ptr(), m, k, xq.data_ptr(), n, ldx, y.data_ptr(), ldy,
+                                   _stream_of(xq, stream))
     _check(st, "qk_mul_mat_vec_x8q")
     return y
 
@@ -494,27 +495,28 @@ def rms_norm(x, weight=None, eps=1e-5, residual=None, out_dtype="f32", y=None, r
         ydtype, row = torch.uint8, k // 32 * X8_BLOCK_BYTES
     else:
         ydtype, row = torch.float32 if ycode == QK_F32 else torch.float16, k
-    _rows_check(x, "x", dtype, n, k)
+    ldx = _rows_check(x, "x", dtype, n, k)
+    r, ldr, s, lds = None, 0, None, 0
     if residual is not None:
-        _rows_check(residual, "residual", dtype, n, k)
+        ldr = _rows_check(residual, "residual", dtype, n, k)
         if residual_out is None:
-            residual_out = torch.empty_like(residual)
+            # (empty_like is the quicker call; of whole rows it gives whole rows)
+            residual_out, lds = torch.empty_like(residual) if ldr == k else x.new_empty((n, k)), k
         else:
-            _rows_check(residual_out, "residual_out", dtype, n, k)
+            lds = _rows_check(residual_out, "residual_out", dtype, n, k)
+        r, s = residual.data_ptr(), residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out without residual")
     if weight is not None:
         _vec_check(weight, "weight", k)
     if y is None:
-        y = torch.empty_like(x) if ydtype is dtype else x.new_empty((n, row), dtype=ydtype)
+        y = torch.empty_like(x) if ydtype is dtype and ldx == k else x.new_empty((n, row), dtype=ydtype)
+        ldy = row
     else:
-        _rows_check(y, "y", ydtype, n, row)
+        ldy = _rows_check(y, "y", ydtype, n, row)
     _on_device(x, y, residual, residual_out, weight)
-    r, ldr, s, lds = None, 0, None, 0
-    if residual is not None:
-        r, ldr, s, lds = residual.data_ptr(), residual.stride(0), residual_out.data_ptr(), residual_out.stride(0)
-    st = load().qk_rms_norm(code, x.data_ptr(), x.stride(0), r, ldr, weight.data_ptr() if weight is not None else None,
-                            eps, n, k, s, lds, ycode, y.data_ptr(), y.stride(0), _stream_of(x, stream))
+    st = load().qk_rms_norm(code, x.data_ptr(), ldx, r, ldr, weight.data_ptr() if weight is not None else None,
+                            eps, n, k, s, lds, ycode, y.data_ptr(), ldy, _stream_of(x, stream))
     _check(st, "qk_rms_norm")
     return y if residual is None else (y, residual_out)
 
@@ -713,17 +715,17 @@ def moe_route(logits, n_used, score="softmax", bias=None, n_groups=1, topk_group
     if not 1 <= n_used <= 64:
         raise ValueError(f"n_used must be 1..64, got {n_used}")
     if ids is None:
-        ids = logits.new_empty((n, n_used), dtype=torch.int32)
+        ids, ld_ids = logits.new_empty((n, n_used), dtype=torch.int32), n_used
     else:
-        _rows_check(ids, "ids", torch.int32, n, n_used)
+        ld_ids = _rows_check(ids, "ids", torch.int32, n, n_used)
     if weights is None:
-        weights = logits.new_empty((n, n_used))
+        weights, ldw = logits.new_empty((n, n_used)), n_used
     else:
-        _rows_check(weights, "weights", torch.float32, n, n_used)
+        ldw = _rows_check(weights, "weights", torch.float32, n, n_used)
     _on_device(logits, ids, weights, bias)
     st = load().qk_moe_route(logits.data_ptr(), logits.stride(0), n, experts, n_used, code,
                              bias.data_ptr() if bias is not None else None, n_groups, topk_groups, group_top,
-                             1 if renorm else 0, scale, ids.data_ptr(), ids.stride(0), weights.data_ptr(),
-                             weights.stride(0), _stream_of(logits, stream))
+                             1 if renorm else 0, scale, ids.data_ptr(), ld_ids, weights.data_ptr(), ldw,
+                             _stream_of(logits, stream))
     _check(st, "qk_moe_route")
     return ids, weights
