@@ -36,7 +36,9 @@ constexpr int64_t kMaxNormRow = int64_t(1) << 30;
 
 // Strides whose products with 32-bit counts stay far below 2^63 bytes.
 bool stride_ok(int64_t ld) { return ld >= 0 && ld <= (int64_t(1) << 27); }
-bool ld_ok(int64_t ld, int64_t len) { return ld >= len && ld <= (int64_t(1) << 31); }
+bool ld_ok(int64_t n, int64_t ld, int64_t len) {
+    return ld >= len && (n <= 1 || ld <= (int64_t(1) << 58) / (n - 1));
+}
 
 struct Range {
     const void *p;
@@ -392,7 +394,7 @@ int qk_rms_norm(int x_dtype, const void *x, int64_t ldx, const void *residual, i
         ldx = ldr = lds = k;
         ldy = yrow;
     }
-    if (!ld_ok(ldx, k) || !ld_ok(ldy, yrow) || (residual && !ld_ok(ldr, k)) || (sum && !ld_ok(lds, k)))
+    if (!ld_ok(n, ldx, k) || !ld_ok(n, ldy, yrow) || (residual && !ld_ok(n, ldr, k)) || (sum && !ld_ok(n, lds, k)))
         return QK_ERR_INVALID_ARG;
     const size_t xe = x_dtype == QK_F32 ? 4 : 2, ye = x8 ? 1 : y_dtype == QK_F32 ? 4 : 2;
     if ((uintptr_t)x % xe != 0 || (uintptr_t)residual % xe != 0 || (uintptr_t)sum % xe != 0 ||
@@ -536,7 +538,8 @@ int qk_moe_route(const float *logits, int64_t ldx, int64_t n_tokens, int64_t n_e
         ldx = n_experts;
         ld_ids = ldw = n_used;
     }
-    if (!ld_ok(ldx, n_experts) || !ld_ok(ld_ids, n_used) || !ld_ok(ldw, n_used)) return QK_ERR_INVALID_ARG;
+    if (!ld_ok(n_tokens, ldx, n_experts) || !ld_ok(n_tokens, ld_ids, n_used) || !ld_ok(n_tokens, ldw, n_used))
+        return QK_ERR_INVALID_ARG;
     if (((uintptr_t)logits | (uintptr_t)bias | (uintptr_t)ids | (uintptr_t)weights) % 4 != 0) return QK_ERR_ALIGNMENT;
     const size_t xb = span_bytes(n_tokens, ldx, n_experts, 4), bb = bias ? (size_t)n_experts * 4 : 0;
     const size_t ib = span_bytes(n_tokens, ld_ids, n_used, 4), wb = span_bytes(n_tokens, ldw, n_used, 4);

@@ -369,7 +369,7 @@ typedef struct qk_kv_cache {
  * of one call must not have the same place.
  *
  *   k, v       fp32; token i, head h at element i*k_tok + h*k_head
- *              (v_tok, v_head), head_dim contiguous elements; strides >= 0
+ *              (v_tok, v_head), head_dim contiguous elements; strides 0..2^27
  *   n_tokens   >= 0 (0 is a no-op); 2*n_tokens*n_heads <= INT32_MAX
  *   table      device int32, n_seqs rows of max_pages ids, stride ld_table
  *   seq        device int32[n_tokens], or NULL: token i is of sequence i
@@ -399,11 +399,12 @@ int qk_kv_store(const qk_kv_cache *cache, const float *k, int64_t k_tok, int64_t
  * that of fp32 arithmetic.
  *
  *   q          fp32; sequence s, head h at element s*q_seq + h*q_head,
- *              head_dim contiguous elements; strides >= 0
+ *              head_dim contiguous elements; strides 0..2^27
  *   n_seqs     >= 0 (0 is a no-op)
  *   n_q_heads  a multiple of the cache's n_heads
- *   table      device int32, n_seqs rows, stride ld_table >= the pages of
- *              max_len tokens (ignored if n_seqs == 1)
+ *   table      device int32, n_seqs rows of the pages of max_len tokens
+ *              (ceil(max_len / page_size); entries that are not followed may
+ *              hold anything), stride ld_table (ignored if n_seqs == 1)
  *   lens       device int32[n_seqs]: tokens in the cache, the new one among them
  *   max_len    1..2^30, no length is above it
  *   window, sinks   >= 0
