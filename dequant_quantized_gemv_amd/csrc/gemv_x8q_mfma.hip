@@ -218,7 +218,8 @@ __global__ __launch_bounds__(64 * W) void gemv_x8q_mfma_kernel(const GemvItem it
                 const u4_t xc = own && in ? sh.codes[b][j & 7][g & 1] : u4_t{0, 0, 0, 0};
                 const i4_t dot = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i4_t, xc), __builtin_bit_cast(i4_t, wv),
                                                                        i4_t{0, 0, 0, 0}, 0, 0, 0);
-                const f4_t dx = *reinterpret_cast<const f4_t *>(&sh.d[in ? b : b0][4 * (g & 1)]);
+                f4_t dx = *reinterpret_cast<const f4_t *>(&sh.d[in ? b : b0][4 * (g & 1)]);
+                if (left < 4 && !in) dx = f4_t{0.0f, 0.0f, 0.0f, 0.0f};  // (an infinite scale times 0 is no 0)
                 const float dw = h2f(dm[p] & 0xFFFFu);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf((float)dot[i], dw * dx[i], acc[i]);

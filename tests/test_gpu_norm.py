@@ -240,6 +240,32 @@ def test_x8q_any_scales_strides_and_alignment(fmt):
         assert_within(y, ref, s, (k // 32 + 8) * U, f"x8q {fmt} {w_off} {ldx}")
 
 
+@pytest.mark.parametrize("fmt", ["q8_0", "q4_1"])
+@pytest.mark.parametrize("nb,n", [(9, 8), (10, 2), (131, 5)])
+def test_x8q_infinite_scale_is_an_infinite_output(fmt, nb, n):
+    """One block of one column with an infinite scale: that column's outputs
+    are infinite with the sign of the block's product, the others as ever.
+    The block is the last of the row, which a pass of four leaves short."""
+    m, k = 37, 32 * nb
+    rng = np.random.default_rng(nb)
+    w = synth.quant_matrix(fmt, m, k, seed=195, tensor_id=nb, d_range=D_RANGE[fmt])
+    q = rng.integers(-127, 128, (n, k))
+    d = rng.uniform(0.1, 0.5, (n, nb)).astype(np.float32)
+    if fmt == "q4_1":
+        q[1, -32:] = 0                      # (its minimum would meet the scale too)
+        q[1, -32] = 1
+    d[1, -1] = np.inf
+    wf = oracle.dequantize_f32(fmt, w, m, k).astype(np.float64).reshape(m, k)
+    block = (q[1, -32:] * wf[:, -32:]).sum(-1)
+    y = _x8q(fmt, w, m, k, _blocks(q, d))
+    assert np.isfinite(np.delete(y, 1, 0)).all()
+    if fmt == "q8_0":
+        sure = np.abs(block) > 0
+        assert np.array_equal(y[1][sure], np.sign(block[sure]) * np.inf)
+    else:
+        assert not np.isfinite(y[1]).any()
+
+
 def test_x8q_nan_scale_and_empty_rows():
     m, k = 20, 128
     w = synth.quant_matrix("q4_0", m, k, seed=9, tensor_id=1, d_range=D_RANGE["q4_0"])
