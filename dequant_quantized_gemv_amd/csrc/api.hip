@@ -128,8 +128,8 @@ Ranges cache_ranges(const qk_kv_cache &c) {
 // tiles.  The lengths are on the device, so the chunk follows from max_len:
 // enough chunks to give every CU two workgroups (one where head_dim leaves room
 // for one wave per SIMD), and at least one tile for each wave of a workgroup.
-// A workgroup's first rows wait for its length, page ids and keys one after
-// another, so more and shorter chunks cost more than their balance gives:
+// Beginning and ending a chunk costs a workgroup several microseconds under
+// load, so more and shorter chunks cost more than their balance gives:
 // 131072 tokens of 8 x 128 in fp16 at 2 / 3 / 4 / 8 / 16 workgroups per CU 100.7 /
 // 101.8 / 105 / 110 / 121 us; 64 sequences of 2048 tokens in 8 bits 57 / - / 63 / 67 /
 // -, of 64..4096 tokens 75 / 74 / 74 / 73 / 74; head_dim 256, 131072 tokens of 2
