@@ -11,6 +11,12 @@
 // exponential and correctly rounded divisions, and the softmax's sum is held in
 // fp64 and rounded once.  Where no bias and no sum of two decides (both
 // scores rise with the logit), the logits themselves are compared.
+//
+// Bound by the choices one after another for few tokens (1 x 128, 8 chosen: 3.1
+// us, of which the launch is 1.6) and by vector instructions for many (about 700 a
+// token: 4096 x 256 in 8 groups 6.9 us, 4096 x 128 4.6 us, their logits 1 us of
+// traffic).  Groups that are segments of 1, 2, 4 .. lanes are scored all at
+// once and ranked by counting (10.7 -> 7.0 us against a wave maximum per group).
 #include "qk_common.h"
 #include "qk_internal.h"
 
