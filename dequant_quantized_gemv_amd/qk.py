@@ -405,12 +405,29 @@ def mul_mat(fmt, w, m, k, x, y=None, stream=None):
 # make them counts: the checks that a well-formed call passes are a few
 # attribute reads, and what refuses is left to the slower helpers above.
 
-def _stream_of(t, stream):
+def _stream_of(t, stream=None):
     """Handle of the caller's stream, or of the current one on t's device."""
     if stream is None:
         import torch
         return torch._C._cuda_getCurrentRawStream(t.get_device())
     return _stream(stream)
+
+
+def _on_stream(stream, t, call, *args):
+    """call(*args) with the caller's stream as the current one of t's device.
+    What a call allocates then comes from the pool of the stream that it runs
+    on; a block of another stream's pool may be in use there still."""
+    import torch
+    device = t.get_device() if isinstance(t, torch.Tensor) else -1
+    handle = _stream(stream)
+    if device < 0 or handle == torch._C._cuda_getCurrentRawStream(device):
+        return call(*args)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    elif stream.device_index != device:
+        raise ValueError(f"stream of device {stream.device_index}, tensors on device {device}")
+    with torch.cuda.stream(stream):
+        return call(*args)
 
 
 def _on_device(*ts):
@@ -442,6 +459,8 @@ def mul_mat_vec_x8q(fmt, w, m, k, xq, y=None, stream=None):
     """As mul_mat_vec_x8, over activations in 8 bits already: xq (n, >= k/32*36)
     uint8, rows of 36-byte blocks as rms_norm(..., out_dtype="x8") gives them."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, xq, mul_mat_vec_x8q, fmt, w, m, k, xq, y)
     _weight_check(fmt, w, m, k)
     if not isinstance(xq, torch.Tensor) or xq.dtype is not torch.uint8:
         raise TypeError("xq must be a uint8 tensor of 8-bit activation blocks")
@@ -457,7 +476,7 @@ def mul_mat_vec_x8q(fmt, w, m, k, xq, y=None, stream=None):
         ldy = _rows_check(y, "y", torch.float32, n, m)
     _on_device(w, xq, y)
     st = load().qk_mul_mat_vec_x8q(_fmt(fmt), w.data_ptr(), m, k, xq.data_ptr(), n, ldx, y.data_ptr(), ldy,
-                                   _stream_of(xq, stream))
+                                   _stream_of(xq))
     _check(st, "qk_mul_mat_vec_x8q")
     return y
 
@@ -476,6 +495,8 @@ def rms_norm(x, weight=None, eps=1e-5, residual=None, out_dtype="f32", y=None, r
     out_dtype "f32", "f16", or "x8" (y uint8 (n, k/32*36), 8-bit activation
     blocks for mul_mat_vec_x8q).  residual_out may be x or residual itself."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, x, rms_norm, x, weight, eps, residual, out_dtype, y, residual_out)
     dtype = x.dtype if isinstance(x, torch.Tensor) else None
     if dtype is torch.float32:
         code = QK_F32
@@ -516,7 +537,7 @@ def rms_norm(x, weight=None, eps=1e-5, residual=None, out_dtype="f32", y=None, r
         ldy = _rows_check(y, "y", ydtype, n, row)
     _on_device(x, y, residual, residual_out, weight)
     st = load().qk_rms_norm(code, x.data_ptr(), ldx, r, ldr, weight.data_ptr() if weight is not None else None,
-                            eps, n, k, s, lds, ycode, y.data_ptr(), ldy, _stream_of(x, stream))
+                            eps, n, k, s, lds, ycode, y.data_ptr(), ldy, _stream_of(x))
     _check(st, "qk_rms_norm")
     return y if residual is None else (y, residual_out)
 
@@ -643,6 +664,9 @@ def attn_decode(cache, q, table, lens, scale=None, window=0, sinks=0, max_len=No
     the split over the cache; a length above it gives NaN.  Returns y (n_seqs,
     n_q_heads, head_dim), fp32 or (out_dtype "f16") fp16."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, q, attn_decode, cache, q, table, lens, scale, window, sinks, max_len, out_dtype, y,
+                          workspace)
     if out_dtype == "f32":
         code, dt = QK_F32, torch.float32
     elif out_dtype == "f16":
@@ -670,14 +694,10 @@ def attn_decode(cache, q, table, lens, scale=None, window=0, sinks=0, max_len=No
     else:
         _heads_check(y, "y", dt, n, heads, dim)
     _on_device(cache.k, q, table, lens, y, workspace)
-    handle = _stream_of(q, stream)
     if workspace is None:
         need = qk_attn_decode_workspace(cache.desc, n, heads, max_len, window, sinks)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-            if stream is not None and handle != _stream_of(q, None):
-                # not to be given out again before the other stream is done with it
-                workspace.record_stream(torch.cuda.ExternalStream(handle, device=q.device))
     elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous uint8 tensor")
     q_head, y_head = (q.stride(1), y.stride(1)) if heads > 1 else (0, 0)
@@ -685,7 +705,7 @@ def attn_decode(cache, q, table, lens, scale=None, window=0, sinks=0, max_len=No
                                table.stride(0), lens.data_ptr(), max_len, dim ** -0.5 if scale is None else scale,
                                window, sinks, code, y.data_ptr(), _row_stride(y), y_head,
                                workspace.data_ptr() if workspace is not None else None,
-                               workspace.numel() if workspace is not None else 0, handle)
+                               workspace.numel() if workspace is not None else 0, _stream_of(q))
     _check(st, "qk_attn_decode")
     return y
 
@@ -702,6 +722,9 @@ def moe_route(logits, n_used, score="softmax", bias=None, n_groups=1, topk_group
     topk_groups best groups of neighbouring experts take part, by the sum of
     their group_top (1 or 2) largest values."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, logits, moe_route, logits, n_used, score, bias, n_groups, topk_groups, group_top,
+                          renorm, scale, ids, weights)
     code = _SCORES.get(score)
     if code is None:
         raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
@@ -726,6 +749,6 @@ def moe_route(logits, n_used, score="softmax", bias=None, n_groups=1, topk_group
     st = load().qk_moe_route(logits.data_ptr(), logits.stride(0), n, experts, n_used, code,
                              bias.data_ptr() if bias is not None else None, n_groups, topk_groups, group_top,
                              1 if renorm else 0, scale, ids.data_ptr(), ld_ids, weights.data_ptr(), ldw,
-                             _stream_of(logits, stream))
+                             _stream_of(logits))
     _check(st, "qk_moe_route")
     return ids, weights
