@@ -260,9 +260,28 @@ def _same_device(*ts):
             raise ValueError(f"tensors on different devices: {dev} and {t.device}")
 
 
+def _on_stream(stream, t, call, *args):
+    """call(*args) with the caller's stream as the current one of t's device.
+    What a call allocates then comes from the pool of the stream that it runs
+    on; a block of another stream's pool may be in use there still."""
+    import torch
+    device = t.get_device() if isinstance(t, torch.Tensor) else -1
+    handle = _stream(stream)
+    if device < 0 or handle == torch._C._cuda_getCurrentRawStream(device):
+        return call(*args)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    elif stream.device_index != device:
+        raise ValueError(f"stream of device {stream.device_index}, tensors on device {device}")
+    with torch.cuda.stream(stream):
+        return call(*args)
+
+
 def dequantize(fmt, w, rows, k, out_dtype="f32", out=None, stream=None):
     """Dequantize a rows x k matrix held as block bytes in a uint8 CUDA tensor."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, w, dequantize, fmt, w, rows, k, out_dtype, out)
     if out_dtype not in ("f32", "f16"):
         raise ValueError(f"out_dtype must be 'f32' or 'f16', got {out_dtype!r}")
     dt = {"f32": (QK_F32, torch.float32), "f16": (QK_F16, torch.float16)}[out_dtype]
@@ -274,7 +293,7 @@ def dequantize(fmt, w, rows, k, out_dtype="f32", out=None, stream=None):
     if tuple(out.shape) != (rows, k) or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous ({rows}, {k}) tensor")
     _same_device(w, out)
-    st = qk_dequantize(fmt, w.data_ptr(), rows, k, dt[0], out.data_ptr(), _stream(stream))
+    st = qk_dequantize(fmt, w.data_ptr(), rows, k, dt[0], out.data_ptr(), _stream(None))
     _check(st, "qk_dequantize")
     return out
 
@@ -298,9 +317,11 @@ def _gemv_args(fmt, w, m, k, x, y):
 def mul_mat_vec(fmt, w, m, k, x, y=None, stream=None):
     """y (n, m) = x (n, k) @ W^T for 1..8 fp32 columns; rows of x and y are the
     ggml columns (contiguous, ldx = x.stride(0), ldy = y.stride(0))."""
+    if stream is not None:
+        return _on_stream(stream, x, mul_mat_vec, fmt, w, m, k, x, y)
     x, y, n = _gemv_args(fmt, w, m, k, x, y)
     st = qk_mul_mat_vec(fmt, w.data_ptr(), m, k, x.data_ptr(), n, x.stride(0),
-                        y.data_ptr(), y.stride(0), _stream(stream))
+                        y.data_ptr(), y.stride(0), _stream(None))
     _check(st, "qk_mul_mat_vec")
     return y
 
@@ -308,9 +329,11 @@ def mul_mat_vec(fmt, w, m, k, x, y=None, stream=None):
 def mul_mat_vec_x8(fmt, w, m, k, x, y=None, stream=None):
     """As mul_mat_vec, with the activations quantized to 8 bits per 32-element
     block inside the kernel and integer dot products (qk_mul_mat_vec_x8)."""
+    if stream is not None:
+        return _on_stream(stream, x, mul_mat_vec_x8, fmt, w, m, k, x, y)
     x, y, n = _gemv_args(fmt, w, m, k, x, y)
     st = qk_mul_mat_vec_x8(fmt, w.data_ptr(), m, k, x.data_ptr(), n, x.stride(0),
-                           y.data_ptr(), y.stride(0), _stream(stream))
+                           y.data_ptr(), y.stride(0), _stream(None))
     _check(st, "qk_mul_mat_vec_x8")
     return y
 
@@ -321,6 +344,8 @@ def mul_mat_vec_batched(fmt, problems, ys=None, stream=None):
     import torch
     if not problems:
         return []
+    if stream is not None:
+        return _on_stream(stream, problems[0][0], mul_mat_vec_batched, fmt, problems, ys)
     if len(problems) > QK_MAX_BATCH:
         raise ValueError(f"at most {QK_MAX_BATCH} problems per launch")
     n = problems[0][3].shape[0] if problems[0][3].dim() == 2 else 1
@@ -337,7 +362,7 @@ def mul_mat_vec_batched(fmt, problems, ys=None, stream=None):
         _same_device(problems[0][0], w)
         tup.append((w.data_ptr(), m, k, x2.data_ptr(), x2.stride(0), y.data_ptr(), y.stride(0)))
     arr = make_items(tup)
-    st = qk_mul_mat_vec_batched(fmt, arr, len(tup), n, _stream(stream))
+    st = qk_mul_mat_vec_batched(fmt, arr, len(tup), n, _stream(None))
     _check(st, "qk_mul_mat_vec_batched")
     return ys
 
@@ -349,6 +374,8 @@ def mul_mat_vec_id(fmt, w, n_experts, m, k, ids, x, y=None, expert_stride=None, 
     (default: packed); ids: int32 CUDA tensor (n_tokens, n_used).  Returns y
     shaped (n_tokens, n_used, m) fp32."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, x, mul_mat_vec_id, fmt, w, n_experts, m, k, ids, x, y, expert_stride)
     if not isinstance(ids, torch.Tensor) or ids.dtype != torch.int32 or ids.dim() != 2 or ids.stride(1) != 1:
         raise TypeError("ids must be int32 (n_tokens, n_used) with contiguous rows")
     n_tokens, n_used = ids.shape
@@ -378,7 +405,7 @@ def mul_mat_vec_id(fmt, w, n_experts, m, k, ids, x, y=None, expert_stride=None, 
     _same_device(w, ids, x, y)
     st = qk_mul_mat_vec_id(fmt, w.data_ptr(), n_experts, expert_stride, m, k, ids.data_ptr(),
                            ids.stride(0), n_used, n_tokens, x.data_ptr(), x_slot, x_tok,
-                           y.data_ptr(), y.stride(1), y.stride(0), _stream(stream))
+                           y.data_ptr(), y.stride(1), y.stride(0), _stream(None))
     _check(st, "qk_mul_mat_vec_id")
     return y
 
@@ -386,6 +413,8 @@ def mul_mat_vec_id(fmt, w, n_experts, m, k, ids, x, y=None, expert_stride=None, 
 def mul_mat(fmt, w, m, k, x, y=None, stream=None):
     """y (n, m) = x (n, k, fp16) @ f16(W)^T on the matrix cores."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, x, mul_mat, fmt, w, m, k, x, y)
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise TypeError("x must be a 2-D float16 tensor (n, k)")
     n = x.shape[0]
@@ -396,7 +425,7 @@ def mul_mat(fmt, w, m, k, x, y=None, stream=None):
     _cols_check(y, "y", torch.float32, n, m)
     _same_device(w, x, y)
     st = qk_mul_mat(fmt, w.data_ptr(), m, k, x.data_ptr(), n, x.stride(0),
-                    y.data_ptr(), y.stride(0), _stream(stream))
+                    y.data_ptr(), y.stride(0), _stream(None))
     _check(st, "qk_mul_mat")
     return y
 
@@ -411,23 +440,6 @@ def _stream_of(t, stream=None):
         import torch
         return torch._C._cuda_getCurrentRawStream(t.get_device())
     return _stream(stream)
-
-
-def _on_stream(stream, t, call, *args):
-    """call(*args) with the caller's stream as the current one of t's device.
-    What a call allocates then comes from the pool of the stream that it runs
-    on; a block of another stream's pool may be in use there still."""
-    import torch
-    device = t.get_device() if isinstance(t, torch.Tensor) else -1
-    handle = _stream(stream)
-    if device < 0 or handle == torch._C._cuda_getCurrentRawStream(device):
-        return call(*args)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
-    elif stream.device_index != device:
-        raise ValueError(f"stream of device {stream.device_index}, tensors on device {device}")
-    with torch.cuda.stream(stream):
-        return call(*args)
 
 
 def _on_device(*ts):

@@ -23,12 +23,19 @@ def _calls():
     g = np.random.default_rng(1)
     x = t.from_numpy(g.standard_normal((2, 64)).astype(np.float32)).cuda()
     w = t.from_numpy(synth.quant_matrix("q4_0", 96, 64, seed=5, tensor_id=1, d_range=D_RANGE["q4_0"])).cuda()
-    x8 = qk.rms_norm(x, out_dtype="x8")
+    xh, x8 = x.half(), qk.rms_norm(x, out_dtype="x8")
     cache = qk.KVCache(*[t.from_numpy(g.standard_normal((256, 2, 16, 64)).astype(np.float16)).cuda() for _ in range(2)])
     table = t.arange(256, dtype=t.int32, device="cuda").view(2, 128)
     q = t.from_numpy(g.standard_normal((2, 4, 64)).astype(np.float32)).cuda()
     lens = t.tensor([2000, 700], dtype=t.int32, device="cuda")
+    ids = t.tensor([[0, 2], [1, 1]], dtype=t.int32, device="cuda")
     return {
+        "dequantize": lambda **k: [qk.dequantize("q4_0", w, 96, 64, **k)],
+        "gemv": lambda **k: [qk.mul_mat_vec("q4_0", w, 96, 64, x, **k)],
+        "gemv x8": lambda **k: [qk.mul_mat_vec_x8("q4_0", w, 96, 64, x, **k)],
+        "batched": lambda **k: qk.mul_mat_vec_batched("q4_0", [(w, 96, 64, x), (w, 32, 64, x)], **k),
+        "id": lambda **k: [qk.mul_mat_vec_id("q4_0", w, 3, 32, 64, ids, x, **k)],
+        "gemm": lambda **k: [qk.mul_mat("q4_0", w, 96, 64, xh, **k)],
         "norm": lambda **k: qk.rms_norm(x, residual=x, **k),
         "norm x8": lambda **k: [qk.rms_norm(x, out_dtype="x8", **k)],
         "x8q": lambda **k: [qk.mul_mat_vec_x8q("q4_0", w, 96, 64, x8, **k)],
@@ -37,7 +44,7 @@ def _calls():
     }
 
 
-@pytest.mark.parametrize("name", ["norm", "norm x8", "x8q", "attn", "route"])
+@pytest.mark.parametrize("name", ["dequantize", "gemv", "gemv x8", "batched", "id", "gemm", "norm", "norm x8", "x8q", "attn", "route"])
 def test_outputs_and_scratch_are_of_the_stream_that_runs(name, monkeypatch):
     t = torch()
     call = _calls()[name]

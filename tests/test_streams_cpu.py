@@ -67,6 +67,12 @@ def record(monkeypatch):
     w, x8 = torch.zeros(64 * 2 * 18, dtype=torch.uint8), torch.zeros(2, 72, dtype=torch.uint8)
     q, lens = torch.zeros(2, 4, 64), torch.zeros(2, dtype=torch.int32)
     r.calls = {
+        "dequantize": lambda s: qk.dequantize("q4_0", w, 64, 64, stream=s),
+        "gemv": lambda s: qk.mul_mat_vec("q4_0", w, 64, 64, f, stream=s),
+        "gemv x8": lambda s: qk.mul_mat_vec_x8("q4_0", w, 64, 64, f, stream=s),
+        "batched": lambda s: qk.mul_mat_vec_batched("q4_0", [(w, 64, 64, f), (w, 32, 64, f)], stream=s),
+        "id": lambda s: qk.mul_mat_vec_id("q4_0", w, 2, 32, 64, i, f, stream=s),
+        "gemm": lambda s: qk.mul_mat("q4_0", w, 64, 64, f.half(), stream=s),
         "norm": lambda s: qk.rms_norm(f, residual=f.clone(), stream=s),
         "norm x8": lambda s: qk.rms_norm(f, out_dtype="x8", stream=s),
         "x8q": lambda s: qk.mul_mat_vec_x8q("q4_0", w, 64, 64, x8, stream=s),
@@ -80,7 +86,8 @@ def record(monkeypatch):
     return r
 
 
-@pytest.mark.parametrize("call", ["norm", "norm x8", "x8q", "attn", "attn y", "route"])
+@pytest.mark.parametrize("call", ["dequantize", "gemv", "gemv x8", "batched", "id", "gemm", "norm", "norm x8", "x8q", "attn",
+                                  "attn y", "route"])
 @pytest.mark.parametrize("handle", [THERE, HERE, 0, None])
 @pytest.mark.parametrize("as_object", [False, True])
 def test_memory_comes_from_the_stream_that_runs(record, call, handle, as_object):
