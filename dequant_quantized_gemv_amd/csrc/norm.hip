@@ -6,11 +6,15 @@
 // registers between the sum of squares and the scaling (rows of more than
 // 16384 elements are read twice).  The sum of squares is held in fp64, which
 // costs nothing beside the loads and cannot overflow, and the row's factor is
-// rounded to fp32 once.
+// rounded to fp32 once; where it lies outside fp32's normal range (rows of
+// subnormal values without eps, rows near the largest value) the elements are
+// moved by a power of two first, which leaves y's digits as they are.
 //
 // Bound by that traffic from about 512 rows: 2048 x 4096 fp32 to 8 bits 20.5 us
 // (110 MB, 5.4 TB/s), fp16 to fp16 12.2 us (67 MB, 5.5 TB/s); below by one row's
 // chain of loads, sums and stores: 1 x 4096 3.2 us, of which the launch is 1.6.
+#include <algorithm>
+
 #include "qk_common.h"
 #include "qk_internal.h"
 
@@ -148,7 +152,12 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_kernel(const NormA
 #pragma unroll
         for (int i = 0; i < T / 64; ++i) ss += part[i];
     }
-    const float f = (float)(1.0 / sqrt(ss / a.k + a.eps));
+    const double factor = 1.0 / sqrt(ss / a.k + a.eps);
+    // (selected, not branched on: the weights' loads stay ahead of this chain,
+    // 1 x 4096 3.4 us; with a branch 3.6, with no such step 3.3)
+    const bool above = factor > 0x1p100, below = factor < 0x1p-100;
+    const float up = above ? 0x1p64f : below ? 0x1p-64f : 1.0f;
+    const float f = (float)(factor * (above ? 0x1p-64 : below ? 0x1p64 : 1.0));
     auto finish = [&](int c, const f4_t &u) {
         if (c >= a.k) return;
         if (s) store4<STREAM>(s, c, a.k, u);
@@ -156,7 +165,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_kernel(const NormA
         f4_t w = {1.0f, 1.0f, 1.0f, 1.0f};
         if (a.w) w = load4(a.w, c, a.k);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = u[i] * f * w[i];
+        for (int i = 0; i < 4; ++i) y[i] = u[i] * up * f * w[i];
         if constexpr (YT == QK_X8) {
             // (k is a multiple of 32: eight lanes hold a block, all of it)
             uint8_t *b = static_cast<uint8_t *>(a.y) + row * a.ldy + (int64_t)(c >> 5) * 36;
@@ -216,6 +225,10 @@ int by_output(int y_dtype, const NormArgs &a, hipStream_t stream) {
 int launch_rms_norm(int x_dtype, const void *x, int64_t ldx, const void *residual, int64_t ldr,
                     const float *weight, double eps, int64_t n, int64_t k, void *sum, int64_t lds,
                     int y_dtype, void *y, int64_t ldy, hipStream_t stream) {
+    // The least mean square of a row that is not zero is 2^-328.  A smaller eps
+    // still makes a zero row zero, as which its factor has to be finite; 2^-382
+    // and less are nothing to any other row.
+    if (eps > 0.0) eps = std::max(eps, 0x1p-382);
     const NormArgs a{x, residual, weight, sum, y, ldx, ldr, lds, ldy, n, (int)k, eps};
     return x_dtype == QK_F16 ? by_output<_Float16>(y_dtype, a, stream) : by_output<float>(y_dtype, a, stream);
 }
