@@ -1,4 +1,5 @@
-"""GPU: qk_rms_norm where its factor leaves fp32's range.  The bound is the norm's own: with u = 2^-24, |y - y64| <= 6 u
+"""GPU: qk_rms_norm where its factor leaves fp32's range, and 8-bit codes that
+meet exact ties.  The bound is the norm's own: with u = 2^-24, |y - y64| <= 6 u
 |y64| for fp32 outputs and half an ulp of the fp16 value more for fp16 ones."""
 import numpy as np
 import pytest
@@ -68,3 +69,23 @@ def test_8_bit_outputs_at_the_ends_of_fp32(scale):
     e = np.ceil(np.log2(np.abs(y).reshape(2, 4, 32).max(-1) / 127))
     assert np.array_equal(d, np.exp2(e).astype(np.float32))
     assert np.array_equal(b[..., 4:].view(np.int8), np.rint(y.reshape(2, 4, 32) / d[..., None]))
+
+
+def test_8_bit_codes_round_ties_to_even():
+    """Elements of magnitude 1 have the factor 1, so y is the weight: blocks
+    of half-whole multiples of their scale."""
+    k = 160
+    w = np.zeros(k, np.float32)
+    w[:32] = np.arange(32) - 15.5                       # largest 15.5, scale 2^-3: quotients whole
+    w[32:64] = np.concatenate([[127.0], np.arange(31) - 15.5])            # scale 1
+    w[64:96] = np.concatenate([[-126.5], np.arange(31) + 80.5])           # scale 1, large codes
+    w[96:128] = np.concatenate([[100.0 * 2.0 ** 40], (np.arange(31) - 15.5) * 2.0 ** 40])
+    w[128:] = np.concatenate([[127.0 * 2.0 ** -130], (np.arange(31) - 15.5) * 2.0 ** -126])
+    x = np.where(np.arange(k) % 3 == 0, -1, 1).astype(np.float32)[None]
+    b = _norm(x, 0.0, "x8", w).reshape(5, 36)
+    d = b[:, :4].copy().view(np.float32)[:, 0].astype(np.float64)
+    quotient = (x[0].astype(np.float64) * w).reshape(5, 32) / d[:, None]
+    ties = np.abs(quotient - np.trunc(quotient)) == 0.5
+    assert ties[1].sum() == 31 and ties[2].sum() == 32 and ties[3].sum() == 31 and ties[4].sum() == 31
+    assert np.array_equal(d, [2.0 ** -3, 1, 1, 2.0 ** 40, 2.0 ** -126])
+    assert np.array_equal(b[:, 4:].view(np.int8), np.rint(quotient))
