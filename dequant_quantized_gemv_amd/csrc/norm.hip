@@ -187,11 +187,28 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_kernel(const NormA
     }
 }
 
+template <typename XT, int YT, int T, int R, bool STREAM>
+int start_parts(const NormArgs &a, hipStream_t stream) {
+    constexpr int ROWS = T <= 64 ? 4 : 1, THREADS = T < 256 ? 256 : T;
+    constexpr int64_t most = max_groups(THREADS) * ROWS;  // rows
+    constexpr int64_t xe = sizeof(XT), ye = YT == QK_X8 ? 1 : YT == QK_F16 ? 2 : 4;
+    for (int64_t row = 0; row < a.n; row += most) {
+        NormArgs p = a;
+        p.n = std::min(a.n - row, most);
+        p.x = static_cast<const uint8_t *>(a.x) + row * a.ldx * xe;
+        if (a.r) p.r = static_cast<const uint8_t *>(a.r) + row * a.ldr * xe;
+        if (a.s) p.s = static_cast<uint8_t *>(a.s) + row * a.lds * xe;
+        p.y = static_cast<uint8_t *>(a.y) + row * a.ldy * ye;
+        const dim3 grid((unsigned)((p.n + ROWS - 1) / ROWS));
+        const int st = launch(rms_norm_kernel<XT, YT, T, R, STREAM>, grid, dim3(THREADS), stream, p);
+        if (st != QK_OK) return st;
+    }
+    return QK_OK;
+}
 template <typename XT, int YT, int T, int R>
 int start(const NormArgs &a, hipStream_t stream) {
-    const dim3 grid((unsigned)(T <= 64 ? (a.n + 3) / 4 : a.n)), block(T < 256 ? 256 : T);
-    if (a.n * a.k > (int64_t(1) << 20)) return launch(rms_norm_kernel<XT, YT, T, R, true>, grid, block, stream, a);
-    return launch(rms_norm_kernel<XT, YT, T, R, false>, grid, block, stream, a);
+    if (a.n * a.k > (int64_t(1) << 20)) return start_parts<XT, YT, T, R, true>(a, stream);
+    return start_parts<XT, YT, T, R, false>(a, stream);
 }
 
 template <typename XT, int YT>

@@ -35,6 +35,10 @@ inline int launch(void (*kern)(KArgs...), dim3 grid, dim3 block, hipStream_t str
     return launch_lds(kern, grid, block, 0, stream, args...);
 }
 
+// Workgroups of one launch: a launch of 2^32 threads or more is refused, so
+// calls that may need more go out in parts.
+constexpr int64_t max_groups(int threads) { return (int64_t(1) << 31) / threads; }
+
 // Compute units of the current device (256 on MI355X if the query fails),
 // queried once per device and kept (launch shapes ask for it on every call).
 inline int device_cus() {
