@@ -29,3 +29,16 @@ def test_norm_of_more_rows_than_a_launch_takes():
     for i in range(0, n, PART):
         a, b = qk.rms_norm(x[i:i + PART], w, residual=x[i:i + PART], out_dtype="x8")
         assert t.equal(y[i:i + PART], a) and t.equal(s[i:i + PART], b), i
+
+
+def test_route_of_more_tokens_than_a_launch_takes():
+    t = torch()
+    n, experts = (1 << 26) + 3, 3
+    g = t.Generator(device="cuda")
+    g.manual_seed(2)
+    x = t.randn(n, experts, device="cuda", generator=g)
+    ids, w = qk.moe_route(x, 2)
+    for i in range(0, n, PART):
+        a, b = qk.moe_route(x[i:i + PART], 2)
+        assert t.equal(ids[i:i + PART], a) and t.equal(w[i:i + PART], b), i
+    assert t.equal(ids[-3:].long(), x[-3:].sort(-1, descending=True)[1][:, :2])
