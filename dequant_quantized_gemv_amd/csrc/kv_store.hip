@@ -9,6 +9,8 @@
 // (49 MB, 5.3 TB/s past the launch) and 11.9 to 13 to 8 bits (41 MB).  Eight elements
 // per lane: 2.5, 10.4 and 11.8, and 6.8 against 6.5 for 1500 tokens to 8 bits;
 // two tokens per group 12.7, key and value rows in groups of their own 13.5.
+#include <algorithm>
+
 #include "attn.h"
 #include "qk_common.h"
 #include "qk_internal.h"
@@ -119,7 +121,25 @@ __global__ __launch_bounds__(256) void kv_store_kernel(const StoreArgs a) {
 template <int GS, bool I8>
 int start(const StoreArgs &a, hipStream_t stream) {
     constexpr int R = 256 / GS;
-    return launch(kv_store_kernel<GS, I8>, dim3((unsigned)((a.tokens + R - 1) / R * a.n_kv)), dim3(256), stream, a);
+    const int64_t most = max_groups(256) / a.n_kv * R;  // tokens of one launch
+    for (int64_t tok = 0; tok < a.tokens; tok += most) {
+        StoreArgs p = a;
+        p.tokens = std::min(a.tokens - tok, most);
+        p.k = a.k + tok * a.k_tok;
+        p.v = a.v + tok * a.v_tok;
+        p.pos = a.pos + tok;
+        if (a.seq) {
+            p.seq = a.seq + tok;
+        } else {
+            // (token i is of sequence i)
+            p.n_seqs = (int)std::max<int64_t>(a.n_seqs - tok, 0);
+            p.table = a.table + (p.n_seqs > 0 ? tok * a.ld_table : 0);
+        }
+        const dim3 grid((unsigned)((p.tokens + R - 1) / R * a.n_kv));
+        const int st = launch(kv_store_kernel<GS, I8>, grid, dim3(256), stream, p);
+        if (st != QK_OK) return st;
+    }
+    return QK_OK;
 }
 
 template <bool I8>

@@ -42,3 +42,31 @@ def test_route_of_more_tokens_than_a_launch_takes():
         a, b = qk.moe_route(x[i:i + PART], 2)
         assert t.equal(ids[i:i + PART], a) and t.equal(w[i:i + PART], b), i
     assert t.equal(ids[-3:].long(), x[-3:].sort(-1, descending=True)[1][:, :2])
+
+
+@pytest.mark.parametrize("with_seq", [True, False])
+def test_store_of_more_rows_than_a_launch_takes(with_seq):
+    """64 heads of 32 elements: 2^23 tokens are 2^32 threads.  All tokens share
+    one row of keys and one of values (strides of 0); most have no place, and
+    the others lie at both ends and where parts of the call may meet."""
+    t = torch()
+    n, heads, dim, page = (1 << 23) + 70, 64, 32, 16
+    places = [0, 1, 31, (1 << 22) - 1, 1 << 22, (1 << 22) + 1, (1 << 22) + 33, (1 << 23) - 1, 1 << 23, n - 2, n - 1]
+    cache = qk.KVCache.empty(3, heads, page, dim)
+    g = t.Generator(device="cuda")
+    g.manual_seed(3)
+    k, v = (t.randn(1, heads, dim, device="cuda", generator=g).expand(n, heads, dim) for _ in range(2))
+    pos = t.full((n,), -1, dtype=t.int32, device="cuda")
+    pos[places] = t.arange(len(places), dtype=t.int32, device="cuda") + 20
+    if with_seq:
+        table = t.tensor([[1, 2]], dtype=t.int32, device="cuda")
+        seq = t.zeros(n, dtype=t.int32, device="cuda")
+    else:
+        table = t.tensor([1, 2], dtype=t.int32, device="cuda").repeat(n, 1)
+        seq = None
+    qk.kv_store(cache, k, v, table, pos, seq=seq)
+    for x, pool in ((k, cache.k), (v, cache.v)):
+        want = t.zeros_like(pool)
+        for i in range(len(places)):
+            want[table[0, (20 + i) // page].item(), :, (20 + i) % page] = x[0].half()
+        assert t.equal(pool, want)
