@@ -38,6 +38,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "attn.h"
 #include "qk_common.h"
 #include "qk_internal.h"
@@ -618,11 +620,26 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
 
 template <int D, bool I8>
 int attn_decode_dim(const AttnArgs &a, bool tiled, hipStream_t stream) {
-    const dim3 grid((unsigned)((int64_t)a.n_seqs * a.n_kv * a.head_tiles * a.nchunks));
-    const int st = tiled ? launch(attn_decode_kernel<D, I8, true>, grid, dim3(64 * kAttnWaves), stream, a)
-                         : launch(attn_decode_kernel<D, I8, false>, grid, dim3(64 * kAttnWaves), stream, a);
-    if (st != QK_OK || a.nchunks == 1) return st;
-    return launch(attn_join_kernel<D>, dim3((unsigned)(a.n_seqs * (int64_t)a.n_heads)), dim3(256), stream, a);
+    // sequences of one launch (a sequence has at most 2^20 query heads, and several
+    // chunks only where all of them together have few workgroups)
+    const int64_t rows = (int64_t)a.n_kv * a.head_tiles * a.nchunks;
+    const int64_t most = max_groups(256) / std::max<int64_t>(rows, a.nchunks > 1 ? a.n_heads : 1);
+    for (int64_t seq = 0; seq < a.n_seqs; seq += most) {
+        AttnArgs p = a;
+        p.n_seqs = (int)std::min<int64_t>(a.n_seqs - seq, most);
+        p.q = a.q + seq * a.q_seq;
+        p.y = static_cast<uint8_t *>(a.y) + seq * a.y_seq * (a.out_f16 ? 2 : 4);
+        p.table = a.table + seq * a.ld_table;
+        p.lens = a.lens + seq;
+        if (a.part) p.part = a.part + seq * a.n_heads * a.nchunks * attn_part_floats(D);
+        const dim3 grid((unsigned)(p.n_seqs * rows));
+        int st = tiled ? launch(attn_decode_kernel<D, I8, true>, grid, dim3(64 * kAttnWaves), stream, p)
+                       : launch(attn_decode_kernel<D, I8, false>, grid, dim3(64 * kAttnWaves), stream, p);
+        if (st == QK_OK && a.nchunks > 1)
+            st = launch(attn_join_kernel<D>, dim3((unsigned)(p.n_seqs * (int64_t)a.n_heads)), dim3(256), stream, p);
+        if (st != QK_OK) return st;
+    }
+    return QK_OK;
 }
 
 template <bool I8>

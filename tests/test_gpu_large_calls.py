@@ -70,3 +70,27 @@ def test_store_of_more_rows_than_a_launch_takes(with_seq):
         for i in range(len(places)):
             want[table[0, (20 + i) // page].item(), :, (20 + i) % page] = x[0].half()
         assert t.equal(pool, want)
+
+
+@pytest.mark.parametrize("kind", ["f16", "i8"])
+def test_attention_of_more_rows_than_a_launch_takes(kind):
+    """2^21 sequences of 8 heads are 2^24 workgroups of 256.  All share a few
+    pages, with lengths of 0 to 16 tokens."""
+    t = torch()
+    n, heads, dim, page, pages = (1 << 21) + 3, 8, 32, 16, 50
+    g = t.Generator(device="cuda")
+    g.manual_seed(4)
+    shape = (pages, heads, page, dim)
+    if kind == "f16":
+        pools = [t.randn(*shape, device="cuda", generator=g).half() for _ in range(2)]
+    else:
+        pools = [t.randint(-127, 128, shape, device="cuda", dtype=t.int8, generator=g) for _ in range(2)]
+        pools += [t.rand(shape[:3], device="cuda", generator=g) * 0.02 for _ in range(2)]
+    cache = qk.KVCache(*pools)
+    q = t.randn(n, heads, dim, device="cuda", generator=g)
+    table = t.randint(0, pages, (n, 1), device="cuda", dtype=t.int32, generator=g)
+    lens = t.randint(0, page + 1, (n,), device="cuda", dtype=t.int32, generator=g)
+    y = qk.attn_decode(cache, q, table, lens)
+    part = 300007
+    for i in range(0, n, part):
+        assert t.equal(y[i:i + part], qk.attn_decode(cache, q[i:i + part], table[i:i + part], lens[i:i + part])), i
