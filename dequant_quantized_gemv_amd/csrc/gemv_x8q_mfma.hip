@@ -32,6 +32,7 @@
 #include "qk_common.h"
 #include "qk_internal.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace qk {
@@ -260,14 +261,28 @@ __global__ __launch_bounds__(64 * W) void gemv_x8q_mfma_kernel(const GemvItem it
     }
 }
 
+template <int FMT, int W, bool ALIGNED>
+int start_parts(const GemvItem &it, int n, hipStream_t stream) {
+    constexpr int most = (int)max_groups(64 * W) * 16;  // rows of one launch
+    for (int64_t row = 0; row < it.m; row += most) {
+        GemvItem p = it;
+        p.w = it.w + row * it.nb * Format<FMT>::kBytes;
+        p.y = it.y + row;
+        p.m = (int)std::min<int64_t>(it.m - row, most);
+        const dim3 grid((unsigned)((p.m + 15) / 16));
+        const int st = launch(gemv_x8q_mfma_kernel<FMT, W, ALIGNED>, grid, dim3(64 * W), stream, p, n);
+        if (st != QK_OK) return st;
+    }
+    return QK_OK;
+}
+
 template <int FMT, bool ALIGNED>
 int start(const GemvItem &it, int n, hipStream_t stream) {
-    const dim3 grid((unsigned)((it.m + 15) / 16));
     // no more waves than the row's blocks need
-    if (it.nb <= 8 * kXmSteps) return launch(gemv_x8q_mfma_kernel<FMT, 1, ALIGNED>, grid, dim3(64), stream, it, n);
-    if (it.nb <= 16 * kXmSteps) return launch(gemv_x8q_mfma_kernel<FMT, 2, ALIGNED>, grid, dim3(128), stream, it, n);
-    if (it.nb <= 32 * kXmSteps) return launch(gemv_x8q_mfma_kernel<FMT, 4, ALIGNED>, grid, dim3(256), stream, it, n);
-    return launch(gemv_x8q_mfma_kernel<FMT, 8, ALIGNED>, grid, dim3(512), stream, it, n);
+    if (it.nb <= 8 * kXmSteps) return start_parts<FMT, 1, ALIGNED>(it, n, stream);
+    if (it.nb <= 16 * kXmSteps) return start_parts<FMT, 2, ALIGNED>(it, n, stream);
+    if (it.nb <= 32 * kXmSteps) return start_parts<FMT, 4, ALIGNED>(it, n, stream);
+    return start_parts<FMT, 8, ALIGNED>(it, n, stream);
 }
 
 template <int FMT>

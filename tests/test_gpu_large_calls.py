@@ -94,3 +94,23 @@ def test_attention_of_more_rows_than_a_launch_takes(kind):
     part = 300007
     for i in range(0, n, part):
         assert t.equal(y[i:i + part], qk.attn_decode(cache, q[i:i + part], table[i:i + part], lens[i:i + part])), i
+
+
+def test_x8q_of_more_rows_than_a_launch_takes():
+    """One block per row, two columns: the matrix-core kernel gives 16 rows a
+    wave, so 2^30 rows are 2^32 threads."""
+    t = torch()
+    m, k = (1 << 30) + 37, 32
+    g = t.Generator(device="cuda")
+    g.manual_seed(5)
+    w = t.empty(m * 18, dtype=t.uint8, device="cuda")
+    for i in range(0, m, PART):
+        b = w[18 * i:18 * (i + PART)]
+        b.random_(0, 256, generator=g)
+        b.view(-1, 18)[:, :2] = t.tensor([0.0078125], dtype=t.float16, device="cuda").view(t.uint8)
+    x = qk.rms_norm(t.randn(2, k, device="cuda", generator=g), out_dtype="x8")
+    y = qk.mul_mat_vec_x8q("q4_0", w, m, k, x)
+    for i in range(0, m, PART):
+        rows = min(PART, m - i)
+        part = qk.mul_mat_vec_x8q("q4_0", w[18 * i:18 * (i + rows)], rows, k, x)
+        assert t.equal(y[:, i:i + rows], part), i
