@@ -123,6 +123,17 @@ Ranges cache_ranges(const qk_kv_cache &c) {
     return out;
 }
 
+// The most 32-token tiles that a sequence of up to max_len tokens can have.
+int64_t attn_tiles(const qk::AttnArgs &a) {
+    const int64_t all = (a.max_len + qk::kAttnTile - 1) / qk::kAttnTile;
+    if (a.window == 0) return all;
+    return std::min<int64_t>(all, (a.sinks + qk::kAttnTile - 1) / qk::kAttnTile +
+                                      (a.window + qk::kAttnTile - 1) / qk::kAttnTile + 1);
+}
+
+// Workgroups that a decode attention is split for (see attn_plan).
+int64_t attn_target(const qk_kv_cache &c) { return (c.head_dim <= 128 ? 2 : 1) * (int64_t)qk::device_cus(); }
+
 // Sizes and the split of a decode attention over the cache's length: the
 // tokens of a sequence go to workgroups in chunks of `chunk_tiles` 32-token
 // tiles.  The lengths are on the device, so the chunk follows from max_len:
@@ -156,13 +167,9 @@ int attn_plan(const qk_kv_cache &c, int64_t n_seqs, int64_t n_q_heads, int64_t m
     a.window = (int)std::min<int64_t>(window, max_len);
     a.sinks = (int)std::min<int64_t>(sinks, max_len);
     if (n_seqs == 0) return QK_OK;
-    // the most tiles a sequence of up to max_len tokens can have
-    int64_t tiles = (max_len + qk::kAttnTile - 1) / qk::kAttnTile;
-    if (a.window > 0)
-        tiles = std::min<int64_t>(tiles, (a.sinks + qk::kAttnTile - 1) / qk::kAttnTile +
-                                             (a.window + qk::kAttnTile - 1) / qk::kAttnTile + 1);
+    const int64_t tiles = attn_tiles(a);
     const int64_t rows = n_seqs * a.n_kv * a.head_tiles;
-    const int64_t target = (c.head_dim <= 128 ? 2 : 1) * (int64_t)qk::device_cus();
+    const int64_t target = attn_target(c);
     int64_t chunk = (tiles * rows + target - 1) / target;
     chunk = std::max<int64_t>(qk::kAttnWaves, (chunk + qk::kAttnWaves - 1) / qk::kAttnWaves * qk::kAttnWaves);
     a.chunk_tiles = (int)std::min<int64_t>(chunk, tiles);
@@ -174,6 +181,19 @@ int attn_plan(const qk_kv_cache &c, int64_t n_seqs, int64_t n_q_heads, int64_t m
 size_t attn_workspace(const qk_kv_cache &c, const qk::AttnArgs &a) {
     if (a.nchunks <= 1) return 0;
     return 4 * (size_t)a.n_seqs * a.n_heads * a.nchunks * (size_t)qk::attn_part_floats((int)c.head_dim);
+}
+
+// The most that attn_workspace() asks for over calls of up to these sizes, so
+// that scratch made once serves a batch that shrinks.  With r < target rows,
+// chunks of at least max(kAttnWaves, tiles * r / target) tiles: a row has at
+// most tiles / kAttnWaves of them rounded up, and all rows at most target + r.
+// (From target rows on there is one chunk a row, and nothing to join.)
+size_t attn_workspace_bound(const qk_kv_cache &c, const qk::AttnArgs &a) {
+    const int64_t tiles = attn_tiles(a), row = (int64_t)a.n_kv * a.head_tiles, target = attn_target(c);
+    if (tiles <= qk::kAttnWaves || row >= target) return 0;
+    const int64_t seqs = std::min<int64_t>(a.n_seqs, (target - 1) / row);
+    const int64_t parts = std::min(seqs * ((tiles + qk::kAttnWaves - 1) / qk::kAttnWaves), target / row + seqs);
+    return 4 * (size_t)parts * a.n_heads * (size_t)qk::attn_part_floats((int)c.head_dim);
 }
 
 }  // namespace
@@ -458,7 +478,7 @@ size_t qk_attn_decode_workspace(const qk_kv_cache *cache, int64_t n_seqs, int64_
     if (check_cache(cache) != QK_OK) return 0;
     qk::AttnArgs a{};
     if (attn_plan(*cache, n_seqs, n_q_heads, max_len, window, sinks, a) != QK_OK) return 0;
-    return attn_workspace(*cache, a);
+    return attn_workspace_bound(*cache, a);
 }
 
 int qk_attn_decode(const qk_kv_cache *cache, const float *q, int64_t q_seq, int64_t q_head,

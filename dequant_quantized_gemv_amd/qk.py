@@ -659,8 +659,9 @@ def kv_store(cache, k, v, table, pos, seq=None, stream=None):
 
 
 def attn_decode_workspace(cache, n_seqs, n_q_heads, max_len, window=0, sinks=0):
-    """Scratch for attn_decode calls of these sizes: a uint8 tensor, or None
-    where none is needed.  One tensor serves one stream at a time."""
+    """Scratch for attn_decode calls of up to these sizes (n_seqs, max_len, and a
+    window and sinks where they are given): a uint8 tensor, or None where none
+    is needed.  One tensor serves one stream at a time."""
     import torch
     need = qk_attn_decode_workspace(cache.desc, n_seqs, n_q_heads, max_len, window, sinks)
     return torch.empty(need, dtype=torch.uint8, device=cache.device) if need else None

@@ -411,9 +411,9 @@ int qk_kv_store(const qk_kv_cache *cache, const float *k, int64_t k_tok, int64_t
  *   y_dtype    QK_F32 or QK_F16; y laid out as q with y_seq, y_head; the rows
  *              must not overlap
  *   workspace  device memory, 16-byte aligned, of the bytes that
- *              qk_attn_decode_workspace gives for the same arguments (NULL if
- *              0); it need not be cleared, and is free for other use once the
- *              enqueued work is done
+ *              qk_attn_decode_workspace gives for these arguments or larger
+ *              ones (NULL if 0); it need not be cleared, and is free for other
+ *              use once the enqueued work is done
  */
 int qk_attn_decode(const qk_kv_cache *cache, const float *q, int64_t q_seq, int64_t q_head,
                    int64_t n_seqs, int64_t n_q_heads, const int32_t *table, int64_t ld_table,
@@ -421,8 +421,10 @@ int qk_attn_decode(const qk_kv_cache *cache, const float *q, int64_t q_seq, int6
                    int y_dtype, void *y, int64_t y_seq, int64_t y_head,
                    void *workspace, size_t workspace_bytes, void *stream);
 
-/* Bytes of workspace that qk_attn_decode needs; 0 where it needs none, and on
- * a bad argument. */
+/* Bytes of workspace that serve qk_attn_decode with up to n_seqs sequences, any
+ * max_len up to the given one and, with a window, any window and sinks up to
+ * the given ones, over this cache and with n_q_heads; 0 where none of these
+ * needs any, and on a bad argument. */
 size_t qk_attn_decode_workspace(const qk_kv_cache *cache, int64_t n_seqs, int64_t n_q_heads,
                                 int64_t max_len, int64_t window, int64_t sinks);
 
