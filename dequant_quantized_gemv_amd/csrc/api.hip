@@ -52,7 +52,7 @@ struct Step {
     int64_t n, stride;
 };
 bool rows_disjoint(int64_t len, std::initializer_list<Step> list) {
-    Step s[3];
+    Step s[4];
     int count = 0;
     for (const Step &x : list)
         if (x.n > 1) s[count++] = x;
@@ -461,10 +461,23 @@ int qk_kv_store(const qk_kv_cache *cache, const float *k, int64_t k_tok, int64_t
             overlaps(r.p, r.n, pos, ib) || (seq && overlaps(r.p, r.n, seq, ib)))
             return QK_ERR_INVALID_ARG;
     }
+    // Keys and values may lie between one another (pages or tokens that hold
+    // both), and so may their scales: then which of the two is one more step.
     const Ranges rs = cache_ranges(c);
     for (size_t i = 0; i < rs.size(); ++i)
-        for (size_t j = 0; j < i; ++j)
-            if (overlaps(rs[i].p, rs[i].n, rs[j].p, rs[j].n)) return QK_ERR_INVALID_ARG;
+        for (size_t j = 0; j < i; ++j) {
+            if (!overlaps(rs[i].p, rs[i].n, rs[j].p, rs[j].n)) continue;
+            const uintptr_t a = (uintptr_t)rs[i].p, b = (uintptr_t)rs[j].p;
+            const int64_t apart = (int64_t)(a > b ? a - b : b - a);
+            const bool rows = i == 1 && j == 0, scales = i == 3 && j == 2;
+            if (rows && rows_disjoint(c.head_dim, {{c.n_pages, c.page_stride}, {c.n_heads, c.head_stride},
+                                                   {c.page_size, c.slot_stride}, {2, apart / (c.type == QK_KV_I8 ? 1 : 2)}}))
+                continue;
+            if (scales && rows_disjoint(1, {{c.n_pages, c.scale_page_stride}, {c.n_heads, c.scale_head_stride},
+                                            {c.page_size, c.scale_slot_stride}, {2, apart / 4}}))
+                continue;
+            return QK_ERR_INVALID_ARG;
+        }
     const qk::StoreArgs a{static_cast<uint8_t *>(c.k), static_cast<uint8_t *>(c.v), c.k_scale, c.v_scale, k, v,
                           table, seq, pos, c.page_stride, c.head_stride, c.slot_stride,
                           c.scale_page_stride, c.scale_head_stride, c.scale_slot_stride,

@@ -374,7 +374,9 @@ typedef struct qk_kv_cache {
  *   table      device int32, n_seqs rows of max_pages ids, stride ld_table
  *   seq        device int32[n_tokens], or NULL: token i is of sequence i
  *   pos        device int32[n_tokens]
- * Errors: QK_ERR_INVALID_ARG also where rows of the pools overlap.
+ * Errors: QK_ERR_INVALID_ARG also where rows of the pools overlap.  Keys and
+ * values may share memory that holds both in turn (pages, tokens or heads of
+ * keys and then values), scales likewise; codes and scales lie apart.
  */
 int qk_kv_store(const qk_kv_cache *cache, const float *k, int64_t k_tok, int64_t k_head,
                 const float *v, int64_t v_tok, int64_t v_head, int64_t n_tokens,
