@@ -379,7 +379,11 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float x = ldexpf(c[i] + d[i], qexp);
+                float x = c[i] + d[i];
+                // a key that overflowed fp16: infinite with the high part, and
+                // NaN with a low part that is 0
+                if constexpr (!I8) x = __builtin_isinf(c[i]) ? c[i] : x;
+                x = ldexpf(x, qexp);
                 if constexpr (I8) x *= kr.sc[4 * u + i];
                 s[4 * u + i] = x;
             }
