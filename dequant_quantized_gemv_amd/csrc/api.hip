@@ -144,7 +144,7 @@ int64_t attn_target(const qk_kv_cache &c) { return (c.head_dim <= 128 ? 2 : 1) *
 // 131072 tokens of 8 x 128 in fp16 at 2 / 3 / 4 / 8 / 16 workgroups per CU 100.7 /
 // 101.8 / 105 / 110 / 121 us; 64 sequences of 2048 tokens in 8 bits 57 / - / 63 / 67 /
 // -, of 64..4096 tokens 75 / 74 / 74 / 73 / 74; head_dim 256, 131072 tokens of 2
-// heads at 1 / 2 61 / 72.
+// heads at 1 / 2 63 / 72.
 int attn_plan(const qk_kv_cache &c, int64_t n_seqs, int64_t n_q_heads, int64_t max_len, int64_t window,
               int64_t sinks, qk::AttnArgs &a) {
     if (n_seqs < 0 || n_seqs > kMaxDim || n_q_heads < 1 || n_q_heads % c.n_heads != 0 || n_q_heads > (1 << 20) ||

@@ -28,10 +28,10 @@
 // per product, too few to hide the fp32 form's time.
 //
 // Bound by the cache's traffic where there are tokens enough: 131072 tokens of
-// 8 heads x 128 in fp16 (537 MB) 100.7 us with the join, 5.3 TB/s; 64 sequences
-// of 2048 tokens in 8 bits (277 MB) 57 us, 4.9 TB/s.  What is left there is the
+// 8 heads x 128 in fp16 (537 MB) 101 us with the join, 5.3 TB/s; 64 sequences
+// of 2048 tokens in 8 bits (277 MB) 55 us, 5.0 TB/s.  What is left there is the
 // start of the workgroups and the join.  A batch of uneven lengths also waits for its longest rows: 64
-// sequences of 64..4096 tokens in 8 bits (283 MB) 74 us.  One sequence of 1000
+// sequences of 64..4096 tokens in 8 bits (283 MB) 73 us.  One sequence of 1000
 // tokens is latency: 6.5 us and 3.8 us for the join, 8.8 us together.
 #pragma once
 

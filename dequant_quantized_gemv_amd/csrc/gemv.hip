@@ -121,13 +121,16 @@ static int launch_x8(int fmt, const void *w, int64_t m, int64_t k, const float *
     const bool fast = ((uintptr_t)d.w % 4) == 0 && (d.nb % 2) == 0;
     if constexpr (X8 == kX8Stored) {
         // The matrix cores cost the same for 1..8 columns, the vector ALU a
-        // column at a time (us, matrix cores against vector ALU): 4096 x 4096
-        // Q4_0 at 2 / 3 / 4 / 8 columns 5.2 / 5.2 / 5.2 / 5.4 against 5.6 / 5.9 / 6.2
-        // / 8.7, Q8_0 6.5 / 6.6 / 6.6 / 6.9 against 6.4 / 6.7 / 7.4 / 9.9; 11008 x 4096
-        // Q4_0 at 2 / 3 / 8 9.5 / 9.4 / 9.6 against 8.9 / 9.7 / 16.5; with too few
-        // rows for the CUs, 1376 x 4096 Q4_0 at 2 / 3 / 4 4.5 / 4.5 / 4.5 against 3.8
-        // / 4.1 / 5.1.  Rows of up to 64 blocks leave the vector kernel's lanes
-        // idle: 4096 x 1376 Q4_0 at 2 3.8 against 5.3.
+        // column at a time (us, matrix cores against vector ALU, weights in no
+        // cache, 2 / 3 columns): 4096 x 4096 Q4_0 5.9 / 5.9 against 6.1 / 6.4, Q8_0
+        // 7.4 / 7.4 against 7.4 / 7.7; 11008 x 4096 Q4_0 10.4 / 10.4 against 10.2 /
+        // 11.1, Q4_1 11.1 / 10.9 against 10.8 / 11.8, Q8_0 15.5 / 14.5 against 16.0 /
+        // 16.6; more rows than that favour the vector ALU again, 14336 x 4096 Q4_0
+        // 13.1 / 12.9 against 11.2 / 12.0; so do too few for the CUs, 1376 x 4096
+        // Q4_0 5.5 / 5.5 against 4.3 / 4.6.  Rows of up to 64 blocks leave the vector
+        // kernel's lanes idle: 4096 x 1376 Q4_0 4.4 / 4.4 against 5.7 / 5.9.  With
+        // weights in the Infinity Cache, 4 / 8 columns of 4096 x 4096 Q4_0 5.2 / 5.4
+        // against 6.2 / 8.7.
         const bool mfma = n >= 4 || (n >= 2 && d.nb <= 64) || (n == 3 && fast && d.m >= 4096);
         if (mfma) return gemv_x8q_mfma(fmt, d, (int)n, stream);
         switch (n) {

@@ -1155,9 +1155,11 @@ constexpr int kGvMaxWgPerCu = QK_GEMV_WG_PER_CU;
 #define QK_GEMV_X8_WG_PER_CU 1
 #endif
 constexpr int kGvX8MaxWgPerCu = QK_GEMV_X8_WG_PER_CU;
-// Stored blocks cost a workgroup a copy and no quantization (1 / 2 / 4 / 8
-// workgroups, one column: Q4_1 11008 x 4096 8.5 / 8.6 / 8.8 / 9.9 us, Q4_0 4096 x
-// 11008 10.4 / 9.0 / 9.0 / 9.0, Q8_0 4096 x 4096 6.3 / 6.1 / 6.1 / 6.1).
+// Stored blocks cost a workgroup a copy and no quantization (1 / 2 / 4
+// workgroups, one column, weights in no cache: Q4_1 11008 x 4096 10.2 / 10.3 /
+// 10.4 us, Q4_0 4096 x 11008 11.6 / 10.4 / 10.3, 14336 x 4096 11.4 / 10.7 / 11.0, 32000
+// x 4096 20.5 / 19.6 / 20.9, 4096 x 4096 5.4 / 5.9 / 5.9, Q8_0 4096 x 4096 7.0 / 6.9 /
+// 7.0; 8 workgroups cost 11008 x 4096 another 1.1).
 #ifndef QK_GEMV_X8Q_WG_PER_CU
 #define QK_GEMV_X8Q_WG_PER_CU 2
 #endif

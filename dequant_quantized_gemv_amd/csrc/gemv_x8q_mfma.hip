@@ -3,7 +3,7 @@
 //
 // Per block of 32 weights the products are whole numbers,
 //   I[col][row] = sum_t x_code[col][t] * w_code[row][t],
-//   y[col][row] += d_w[row] * (d_x[col] * I)   (+ m_w[row] * (d_x[col] * sum_t x_code))
+//   y[col][row] += d_w[row] * d_x[col] * I   (+ m_w[row] * (d_x[col] * sum_t x_code))
 // in fp32.  One v_mfma_i32_16x16x64_i8 makes two blocks for 16 rows and 8
 // columns: the left operand's rows 0..7 hold the columns' codes of the first
 // block and zeros for the second, rows 8..15 the other way round.  The weights
@@ -22,12 +22,19 @@
 // one pass of its waves, so all of its weights are on their way while the
 // activations are staged.
 //
-// Bound by the weights' traffic and the launch: 11008 x 4096 at 8 columns, Q4_1
-// 10.6 us (28.6 MB; the kernel of gemv_impl.h 16.9), Q4_0 9.6 (16.5), Q8_0 13.4
-// (18.8).  Two steps of four blocks per wave in flight leave registers for
-// three workgroups per CU, which is one round of the 688 that 11008 rows are:
-// four steps took 11.8 us.  One block per product, whose results fill half of
-// the lanes, took 10.9 (VALU bound: 26 instructions a block against 12).
+// 11008 x 4096 at 8 columns, weights in no cache: Q4_1 12.3 us (28.2 MB; the
+// kernel of gemv_impl.h, which quantizes them too, 18.7), Q4_0 11.5 (19.7), Q8_0
+// 15.9 (23.7), Q5_0 12.5, Q5_1 12.7; with the weights in the Infinity Cache Q4_1
+// 10.6.  That is not the weights' traffic, which a plain read moves in 5.5:
+// a workgroup stages all columns (36 KB) for 16 rows (40 KB of Q4_1), so that
+// half of what it moves is activations.
+// Steps of four blocks per wave in flight, 1 / 2 / 4 (weights in no cache, 8
+// columns): Q4_0 4096 x 4096 7.0 / 6.2 / 6.6 us, 1376 x 4096 6.8 / 5.8 / 6.2, 4096 x
+// 11008 14.7 / 12.8 / 13.3; tall matrices gain a little with one step, which leaves
+// room for more workgroups on a CU (Q4_1 11008 x 4096 11.3 / 12.3 / 13.1, Q4_0 32000 x
+// 4096 25.3 / 25.8 / 27.8).  One block per product, whose results fill half of the
+// lanes, costs 26 vector instructions a block against 12 (Q4_1 11008 x 4096 10.9
+// against 10.6 us, weights in the Infinity Cache).
 #include "gemv.h"
 #include "qk_common.h"
 #include "qk_internal.h"
@@ -58,8 +65,8 @@ template <int WINDOW> struct XmShared {
 
 // The dwords that lane (g, j) reads of block g of row j: the block's own, or
 // for 18-, 22- and 34-byte blocks the aligned ones that hold it (a 2-byte
-// aligned 16-byte load costs half the rate: 11008 x 4096 at 8 columns Q4_0
-// 13.1 -> 9.6 us, Q8_0 19.4 -> 13.4).  Blocks begin at a dword or, every second one, in
+// aligned 16-byte load costs half the rate: 11008 x 4096 at 8 columns, weights
+// in the Infinity Cache, Q4_0 13.1 -> 9.6 us, Q8_0 19.4 -> 13.4).  Blocks begin at a dword or, every second one, in
 // its middle.
 template <int FMT> constexpr int kXmDwords = (Format<FMT>::kBytes + 3) / 4;
 

@@ -5,8 +5,8 @@
 // elements), four elements of each per lane: a row is read once, the 8-bit
 // scale's maximum is a few lane exchanges, and one lookup serves both rows.
 // Bound by the traffic of the rows, at decode sizes by the launch and the
-// chain of lookups: 64 tokens of 8 x 128 take 2.4 us to fp16, 4000 take 10.9
-// (49 MB, 5.3 TB/s past the launch) and 11.9 to 13 to 8 bits (41 MB).  Eight elements
+// chain of lookups: 64 tokens of 8 x 128 take 2.5 us to fp16 and 3.3 to 8 bits,
+// 4000 take 10.6 (49 MB, 5.4 TB/s past the launch) and 12.9 to 8 bits (41 MB).  Eight elements
 // per lane: 2.5, 10.4 and 11.8, and 6.8 against 6.5 for 1500 tokens to 8 bits;
 // two tokens per group 12.7, key and value rows in groups of their own 13.5.
 #include <algorithm>

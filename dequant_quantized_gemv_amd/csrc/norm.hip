@@ -11,8 +11,8 @@
 // moved by a power of two first, which leaves y's digits as they are.
 //
 // Bound by that traffic from about 512 rows: 2048 x 4096 fp32 to 8 bits 20.5 us
-// (110 MB, 5.4 TB/s), fp16 to fp16 12.2 us (67 MB, 5.5 TB/s); below by one row's
-// chain of loads, sums and stores: 1 x 4096 3.2 us, of which the launch is 1.6.
+// (110 MB, 5.4 TB/s), fp16 to fp16 12.6 us (67 MB, 5.3 TB/s); below by one row's
+// chain of loads, sums and stores: 1 x 4096 3.4 us, of which the launch is 1.6.
 #include <algorithm>
 
 #include "qk_common.h"
@@ -215,7 +215,7 @@ template <typename XT, int YT>
 int run(const NormArgs &a, hipStream_t stream) {
     const int64_t n = a.n;
     // Up to two rows per CU a row has more threads, so that the chain of one
-    // thread's loads and adds is short (1 x 4096 4.5 -> 3.3 us, 256 x 4096 to
+    // thread's loads and adds is short (1 x 4096 4.5 -> 3.4 us, 256 x 4096 to
     // 8 bits 7.3 -> 5.4); beyond, fewer threads leave more rows to a CU (2048 x
     // 4096 to 8 bits 24.4 us against 26.0).
     const bool wide = n <= 2 * (int64_t)device_cus();
