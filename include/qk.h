@@ -188,7 +188,8 @@ int qk_mul_mat_vec_x8(int fmt, const void *w, int64_t m, int64_t k,
  * qk_mul_mat_vec_x8q - qk_mul_mat_vec_x8 over activations that are in 8 bits
  * already: x is n columns of k/32 QK_X8 blocks (fp32 scale, 32 int8 codes),
  * as qk_rms_norm writes them; several products of one vector then share one
- * quantization.  Any scale and codes -128..127 are taken.  With the blocks that
+ * quantization.  Any scale and codes -128..127 are taken (the product of a
+ * weight's and an activation's scale is rounded to fp32).  With the blocks that
  * qk_mul_mat_vec_x8 makes of the same activations the outputs of one column
  * are the same, bit for bit; more columns may run on the matrix cores (exact
  * integer products, fp32 sums over the blocks in another order), and the two
