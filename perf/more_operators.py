@@ -266,7 +266,7 @@ def prepare(c, seed):
             s["cache"] = qk.KVCache(s["kc"], s["vc"], s["ks"], s["vs"])
         if op == "attn":
             s["scratch"] = qk.attn_decode_shared_workspace(s["cache"], c["seqs"], c["q_heads"], c["groups"],
-                                                           c["shared"] + c["tail"], c["shared"])
+                                                           c["shared"] + c["tail"], c["shared"], c["tail"])
         elif op == "fork":
             s["scratch"] = qk.kv_pages_workspace(c["rows"], s["pages"])
         elif op == "compact":
@@ -434,8 +434,8 @@ def _own(s):
         return qk.kv_compact(s["table"], s["lens"], c["page"], c["pages"], workspace=s["scratch"])
     if op == "attn":
         return qk.attn_decode_shared(s["cache"], s["q"], s["table"], s["lens"], s["starts"], s["shared"], s["scale"],
-                                     max_len=c["shared"] + c["tail"], max_shared=c["shared"], out_dtype=c["out"],
-                                     workspace=s["scratch"])
+                                     max_len=c["shared"] + c["tail"], max_shared=c["shared"], max_own=c["tail"],
+                                     out_dtype=c["out"], workspace=s["scratch"])
     return qk.token_logprobs(s["x"], s["ids"], top=c["top"], scale=c["scale"], workspace=s["scratch"])
 
 
