@@ -9,6 +9,8 @@
 #include <initializer_list>
 
 #include "attn.h"
+#include "kv_pages.h"
+#include "logprobs.h"
 #include "qk.h"
 #include "qk_common.h"
 #include "qk_internal.h"
@@ -121,6 +123,33 @@ Ranges cache_ranges(const qk_kv_cache &c) {
         out.count = 4;
     }
     return out;
+}
+
+// Whether a (checked) cache can be written to: no element of its pools lies on
+// another.  Keys and values may lie between one another (pages or tokens that
+// hold both), and so may their scales: then which of the two is one more step.
+bool cache_writable(const qk_kv_cache &c) {
+    if (!rows_disjoint(c.head_dim, {{c.n_pages, c.page_stride}, {c.n_heads, c.head_stride}, {c.page_size, c.slot_stride}}))
+        return false;
+    if (c.type == QK_KV_I8 &&
+        !rows_disjoint(1, {{c.n_pages, c.scale_page_stride}, {c.n_heads, c.scale_head_stride}, {c.page_size, c.scale_slot_stride}}))
+        return false;
+    const Ranges rs = cache_ranges(c);
+    for (size_t i = 0; i < rs.size(); ++i)
+        for (size_t j = 0; j < i; ++j) {
+            if (!overlaps(rs[i].p, rs[i].n, rs[j].p, rs[j].n)) continue;
+            const uintptr_t a = (uintptr_t)rs[i].p, b = (uintptr_t)rs[j].p;
+            const int64_t apart = (int64_t)(a > b ? a - b : b - a);
+            const bool rows = i == 1 && j == 0, scales = i == 3 && j == 2;
+            if (rows && rows_disjoint(c.head_dim, {{c.n_pages, c.page_stride}, {c.n_heads, c.head_stride},
+                                                   {c.page_size, c.slot_stride}, {2, apart / (c.type == QK_KV_I8 ? 1 : 2)}}))
+                continue;
+            if (scales && rows_disjoint(1, {{c.n_pages, c.scale_page_stride}, {c.n_heads, c.scale_head_stride},
+                                            {c.page_size, c.scale_slot_stride}, {2, apart / 4}}))
+                continue;
+            return false;
+        }
+    return true;
 }
 
 // The most 32-token tiles that a sequence of up to max_len tokens can have.
@@ -443,11 +472,7 @@ int qk_kv_store(const qk_kv_cache *cache, const float *k, int64_t k_tok, int64_t
     if (n_tokens < 0 || n_seqs < 0 || max_pages < 0) return QK_ERR_INVALID_ARG;
     if (n_tokens == 0) return QK_OK;
     if (n_tokens > kMaxDim / (2 * c.n_heads) || n_seqs > kMaxDim || max_pages > kMaxDim) return QK_ERR_INVALID_ARG;
-    if (!rows_disjoint(c.head_dim, {{c.n_pages, c.page_stride}, {c.n_heads, c.head_stride}, {c.page_size, c.slot_stride}}))
-        return QK_ERR_INVALID_ARG;
-    if (c.type == QK_KV_I8 &&
-        !rows_disjoint(1, {{c.n_pages, c.scale_page_stride}, {c.n_heads, c.scale_head_stride}, {c.page_size, c.scale_slot_stride}}))
-        return QK_ERR_INVALID_ARG;
+    if (!cache_writable(c)) return QK_ERR_INVALID_ARG;
     if (k == nullptr || v == nullptr || pos == nullptr || table == nullptr) return QK_ERR_INVALID_ARG;
     if (n_seqs <= 1) ld_table = max_pages;
     if (ld_table < max_pages || !stride_ok(ld_table)) return QK_ERR_INVALID_ARG;
@@ -461,23 +486,6 @@ int qk_kv_store(const qk_kv_cache *cache, const float *k, int64_t k_tok, int64_t
             overlaps(r.p, r.n, pos, ib) || (seq && overlaps(r.p, r.n, seq, ib)))
             return QK_ERR_INVALID_ARG;
     }
-    // Keys and values may lie between one another (pages or tokens that hold
-    // both), and so may their scales: then which of the two is one more step.
-    const Ranges rs = cache_ranges(c);
-    for (size_t i = 0; i < rs.size(); ++i)
-        for (size_t j = 0; j < i; ++j) {
-            if (!overlaps(rs[i].p, rs[i].n, rs[j].p, rs[j].n)) continue;
-            const uintptr_t a = (uintptr_t)rs[i].p, b = (uintptr_t)rs[j].p;
-            const int64_t apart = (int64_t)(a > b ? a - b : b - a);
-            const bool rows = i == 1 && j == 0, scales = i == 3 && j == 2;
-            if (rows && rows_disjoint(c.head_dim, {{c.n_pages, c.page_stride}, {c.n_heads, c.head_stride},
-                                                   {c.page_size, c.slot_stride}, {2, apart / (c.type == QK_KV_I8 ? 1 : 2)}}))
-                continue;
-            if (scales && rows_disjoint(1, {{c.n_pages, c.scale_page_stride}, {c.n_heads, c.scale_head_stride},
-                                            {c.page_size, c.scale_slot_stride}, {2, apart / 4}}))
-                continue;
-            return QK_ERR_INVALID_ARG;
-        }
     const qk::StoreArgs a{static_cast<uint8_t *>(c.k), static_cast<uint8_t *>(c.v), c.k_scale, c.v_scale, k, v,
                           table, seq, pos, c.page_stride, c.head_stride, c.slot_stride,
                           c.scale_page_stride, c.scale_head_stride, c.scale_slot_stride,
@@ -582,6 +590,207 @@ int qk_moe_route(const float *logits, int64_t ldx, int64_t n_tokens, int64_t n_e
     return qk::launch_moe_route(logits, ldx, n_tokens, n_experts, n_used, score == QK_SIGMOID, bias, n_groups,
                                 topk_groups, group_top, renorm != 0, scale, ids, ld_ids, weights, ldw,
                                 static_cast<hipStream_t>(stream));
+}
+
+// One plane of a cache's pages as runs of bytes, joined where they lie back to back.
+static qk::CopyPlane copy_plane(void *base, int64_t es, int64_t elems, int64_t page, int64_t n_heads, int64_t head,
+                                int64_t n_slots, int64_t slot) {
+    qk::CopyPlane p{};
+    p.base = static_cast<uint8_t *>(base);
+    p.page_stride = page * es;
+    p.bytes = elems * n_heads * n_slots * es;
+    int64_t run = elems * es, n[2] = {n_heads, n_slots}, stride[2] = {head * es, slot * es};
+    if (n[0] == 1 || (n[1] > 1 && stride[1] < stride[0])) {
+        std::swap(n[0], n[1]);
+        std::swap(stride[0], stride[1]);
+    }
+    if (n[0] == 1 || stride[0] == run) {
+        run *= n[0];
+        n[0] = n[1];
+        stride[0] = stride[1];
+        n[1] = 1;
+        stride[1] = 0;
+        if (n[0] == 1 || stride[0] == run) {
+            run *= n[0];
+            n[0] = 1;
+            stride[0] = 0;
+        }
+    }
+    p.run = run == p.bytes ? 0 : (uint32_t)run;
+    p.inner = (uint32_t)n[0];
+    p.inner_stride = stride[0];
+    p.outer_stride = n[1] > 1 ? stride[1] : 0;
+    return p;
+}
+
+int qk_kv_copy(const qk_kv_cache *cache, const int32_t *src, const int32_t *dst, int64_t n, void *stream) {
+    const int st = check_cache(cache);
+    if (st != QK_OK) return st;
+    const qk_kv_cache &c = *cache;
+    if (n < 0 || n > kMaxDim) return QK_ERR_INVALID_ARG;
+    if (n == 0) return QK_OK;
+    if (!cache_writable(c) || src == nullptr || dst == nullptr) return QK_ERR_INVALID_ARG;
+    if (((uintptr_t)src | (uintptr_t)dst) % 4 != 0) return QK_ERR_ALIGNMENT;
+    for (const Range &r : cache_ranges(c))
+        if (overlaps(r.p, r.n, src, 4 * (size_t)n) || overlaps(r.p, r.n, dst, 4 * (size_t)n)) return QK_ERR_INVALID_ARG;
+    qk::CopyArgs a{};
+    const int64_t es = c.type == QK_KV_I8 ? 1 : 2;
+    a.plane[0] = copy_plane(c.k, es, c.head_dim, c.page_stride, c.n_heads, c.head_stride, c.page_size, c.slot_stride);
+    a.plane[1] = copy_plane(c.v, es, c.head_dim, c.page_stride, c.n_heads, c.head_stride, c.page_size, c.slot_stride);
+    a.planes = 2;
+    if (c.type == QK_KV_I8) {
+        a.plane[2] = copy_plane(c.k_scale, 4, 1, c.scale_page_stride, c.n_heads, c.scale_head_stride, c.page_size, c.scale_slot_stride);
+        a.plane[3] = copy_plane(c.v_scale, 4, 1, c.scale_page_stride, c.n_heads, c.scale_head_stride, c.page_size, c.scale_slot_stride);
+        a.planes = 4;
+    }
+    a.src = src;
+    a.dst = dst;
+    a.n = n;
+    a.n_pages = (int)c.n_pages;
+    return qk::launch_kv_copy(a, static_cast<hipStream_t>(stream));
+}
+
+static bool pages_sizes_ok(int64_t n_rows, int64_t pages, int64_t page_size, int64_t n_pages) {
+    return n_rows >= 0 && n_rows <= kMaxDim && pages >= 0 && pages <= (int64_t(1) << 30) && page_size >= 1 &&
+           page_size <= (1 << 20) && n_pages >= 1 && n_pages <= kMaxDim && (pages == 0 || n_rows <= kMaxDim / pages);
+}
+
+size_t qk_kv_pages_workspace(int64_t n_rows, int64_t n_pages) {
+    if (!pages_sizes_ok(n_rows, 0, 1, n_pages)) return 0;
+    return (4 * (size_t)qk::pages_ws_words(n_rows, n_pages) + 15) / 16 * 16;
+}
+
+int qk_kv_fork(const int32_t *table, int64_t ld_table, const int32_t *lens, int64_t n_rows, int64_t in_pages,
+               const int32_t *parent, const int32_t *new_lens, int64_t n_new, int64_t out_pages,
+               int64_t page_size, int64_t n_pages, int32_t *out, int64_t ld_out, int32_t *src, int32_t *dst,
+               int32_t *missing, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!pages_sizes_ok(n_rows, 0, page_size, n_pages) || !pages_sizes_ok(n_new, in_pages, page_size, n_pages) ||
+        !pages_sizes_ok(n_new, out_pages, page_size, n_pages))
+        return QK_ERR_INVALID_ARG;
+    if (missing == nullptr || workspace == nullptr) return QK_ERR_INVALID_ARG;
+    if (n_rows > 0 && (lens == nullptr || (in_pages > 0 && table == nullptr))) return QK_ERR_INVALID_ARG;
+    if (n_new > 0 && (new_lens == nullptr || src == nullptr || dst == nullptr || (out_pages > 0 && out == nullptr)))
+        return QK_ERR_INVALID_ARG;
+    if (n_rows <= 1) ld_table = in_pages;
+    if (n_new <= 1) ld_out = out_pages;
+    if (ld_table < in_pages || ld_out < out_pages || !stride_ok(ld_table - in_pages) || !stride_ok(ld_out - out_pages)) return QK_ERR_INVALID_ARG;
+    if (((uintptr_t)table | (uintptr_t)lens | (uintptr_t)parent | (uintptr_t)new_lens | (uintptr_t)out | (uintptr_t)src |
+         (uintptr_t)dst | (uintptr_t)missing) % 4 != 0 || (uintptr_t)workspace % 16 != 0)
+        return QK_ERR_ALIGNMENT;
+    const size_t need = qk_kv_pages_workspace(n_new, n_pages);
+    if (workspace_bytes < need) return QK_ERR_INVALID_ARG;
+    const size_t rows = 4 * (size_t)n_new;
+    const Range in[] = {{table, span_bytes(n_rows, ld_table, in_pages, 4)}, {lens, 4 * (size_t)n_rows},
+                        {parent, parent ? rows : 0}, {new_lens, rows}};
+    const Range outs[] = {{out, span_bytes(n_new, ld_out, out_pages, 4)}, {src, rows}, {dst, rows}, {missing, 4}, {workspace, need}};
+    const bool in_place = out == table && parent == nullptr && n_new == n_rows && out_pages == in_pages && ld_out == ld_table;
+    for (size_t i = 0; i < 5; ++i) {
+        for (size_t j = 0; j < i; ++j)
+            if (overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return QK_ERR_INVALID_ARG;
+        for (size_t j = 0; j < 4; ++j)
+            if (overlaps(outs[i].p, outs[i].n, in[j].p, in[j].n) && !(in_place && i == 0 && j == 0)) return QK_ERR_INVALID_ARG;
+    }
+    const qk::ForkArgs a{table, lens, parent, new_lens, out, src, dst, missing, ld_table, ld_out, (int)n_rows, (int)n_new,
+                         (int)in_pages, (int)out_pages, (int)page_size, (int)n_pages, static_cast<uint32_t *>(workspace)};
+    return qk::launch_kv_fork(a, static_cast<hipStream_t>(stream));
+}
+
+int qk_kv_compact(const int32_t *table, int64_t ld_table, const int32_t *lens, int64_t n_rows, int64_t max_pages,
+                  int64_t page_size, int64_t n_pages, int32_t *out, int64_t ld_out, int32_t *src, int32_t *dst,
+                  int32_t *live, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!pages_sizes_ok(n_rows, max_pages, page_size, n_pages)) return QK_ERR_INVALID_ARG;
+    if (live == nullptr || workspace == nullptr || (n_pages > 1 && (src == nullptr || dst == nullptr))) return QK_ERR_INVALID_ARG;
+    if (n_rows > 0 && (lens == nullptr || (max_pages > 0 && (table == nullptr || out == nullptr)))) return QK_ERR_INVALID_ARG;
+    if (n_rows <= 1) ld_table = ld_out = max_pages;
+    if (ld_table < max_pages || ld_out < max_pages || !stride_ok(ld_table - max_pages) || !stride_ok(ld_out - max_pages)) return QK_ERR_INVALID_ARG;
+    if (((uintptr_t)table | (uintptr_t)lens | (uintptr_t)out | (uintptr_t)src | (uintptr_t)dst | (uintptr_t)live) % 4 != 0 ||
+        (uintptr_t)workspace % 16 != 0)
+        return QK_ERR_ALIGNMENT;
+    const size_t need = qk_kv_pages_workspace(n_rows, n_pages);
+    if (workspace_bytes < need) return QK_ERR_INVALID_ARG;
+    const size_t moves = 4 * (size_t)(n_pages / 2);
+    const Range in[] = {{table, span_bytes(n_rows, ld_table, max_pages, 4)}, {lens, 4 * (size_t)n_rows}};
+    const Range outs[] = {{out, span_bytes(n_rows, ld_out, max_pages, 4)}, {src, moves}, {dst, moves}, {live, 4}, {workspace, need}};
+    for (size_t i = 0; i < 5; ++i) {
+        for (size_t j = 0; j < i; ++j)
+            if (overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return QK_ERR_INVALID_ARG;
+        for (size_t j = 0; j < 2; ++j)
+            if (overlaps(outs[i].p, outs[i].n, in[j].p, in[j].n) && !(i == 0 && j == 0 && out == table && ld_out == ld_table))
+                return QK_ERR_INVALID_ARG;
+    }
+    const qk::CompactArgs a{table, lens, out, src, dst, live, ld_table, ld_out, (int)n_rows, (int)max_pages, (int)page_size,
+                            (int)n_pages, static_cast<uint32_t *>(workspace)};
+    return qk::launch_kv_compact(a, static_cast<hipStream_t>(stream));
+}
+
+// Bytes of a part's figures and its best.
+static size_t logp_part_bytes(int64_t top) { return 16 + 8 * (size_t)top; }
+
+size_t qk_token_logprobs_workspace(int64_t n, int64_t vocab, int64_t top) {
+    if (n < 0 || n > kMaxDim || vocab < 1 || vocab > (1 << 30) || top < 0 || top > qk::kLogpMost) return 0;
+    return (size_t)qk::logp_parts_bound(n, vocab, qk::device_cus()) * logp_part_bytes(top);
+}
+
+int qk_token_logprobs(int x_dtype, const void *logits, int64_t ldx, int64_t n, int64_t vocab, float scale,
+                      const int32_t *ids, int64_t ld_ids, int64_t n_ids, float *logprobs, int64_t ld_logprobs,
+                      float *entropy, int64_t top, int32_t *best_ids, int64_t ld_best_ids, float *best, int64_t ld_best,
+                      void *workspace, size_t workspace_bytes, void *stream) {
+    if (x_dtype != QK_F32 && x_dtype != QK_F16) return QK_ERR_UNSUPPORTED;
+    if (n < 0 || vocab < 1 || vocab > (1 << 30) || n_ids < 0 || n_ids > (1 << 20) || top < 0 || top > qk::kLogpMost ||
+        top > vocab || !(scale > 0.0f) || scale > 3.402823466e38f)
+        return QK_ERR_INVALID_ARG;
+    if (n == 0) return QK_OK;
+    if (n > kMaxDim || logits == nullptr || (n_ids > 0 && (ids == nullptr || logprobs == nullptr)) ||
+        (top > 0 && (best_ids == nullptr || best == nullptr)))
+        return QK_ERR_INVALID_ARG;
+    if (n == 1) {
+        ldx = vocab;
+        ld_ids = ld_logprobs = n_ids;
+        ld_best_ids = ld_best = top;
+    }
+    if (!ld_ok(n, ldx, vocab) || (n_ids > 0 && (!ld_ok(n, ld_ids, n_ids) || !ld_ok(n, ld_logprobs, n_ids))) ||
+        (top > 0 && (!ld_ok(n, ld_best_ids, top) || !ld_ok(n, ld_best, top))))
+        return QK_ERR_INVALID_ARG;
+    const size_t es = x_dtype == QK_F32 ? 4 : 2;
+    if ((uintptr_t)logits % es != 0 || ((uintptr_t)ids | (uintptr_t)logprobs | (uintptr_t)entropy | (uintptr_t)best_ids |
+                                        (uintptr_t)best) % 4 != 0 || (uintptr_t)workspace % 16 != 0)
+        return QK_ERR_ALIGNMENT;
+    const int each = qk::logp_each(n, vocab, qk::device_cus());
+    const int64_t parts = qk::logp_parts(vocab, each);
+    const size_t need = parts > 1 ? (size_t)n * parts * logp_part_bytes(top) : 0;
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return QK_ERR_INVALID_ARG;
+    const Range in[] = {{logits, span_bytes(n, ldx, vocab, es)}, {ids, span_bytes(n, ld_ids, n_ids, 4)}};
+    const Range outs[] = {{logprobs, span_bytes(n, ld_logprobs, n_ids, 4)}, {entropy, entropy ? 4 * (size_t)n : 0},
+                          {best_ids, span_bytes(n, ld_best_ids, top, 4)}, {best, span_bytes(n, ld_best, top, 4)}, {workspace, need}};
+    for (size_t i = 0; i < 5; ++i) {
+        for (size_t j = 0; j < i; ++j)
+            if (overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return QK_ERR_INVALID_ARG;
+        for (size_t j = 0; j < 2; ++j)
+            if (overlaps(outs[i].p, outs[i].n, in[j].p, in[j].n)) return QK_ERR_INVALID_ARG;
+    }
+    qk::LogpArgs a{};
+    a.x = logits;
+    a.ids = ids;
+    a.lp = logprobs;
+    a.entropy = entropy;
+    a.best = best;
+    a.best_ids = best_ids;
+    a.ldx = ldx;
+    a.ld_ids = ld_ids;
+    a.ld_lp = ld_logprobs;
+    a.ld_best_ids = ld_best_ids;
+    a.ld_best = ld_best;
+    a.n = n;
+    a.vocab = (int)vocab;
+    a.n_ids = (int)n_ids;
+    a.top = (int)top;
+    a.parts = (int)parts;
+    a.scale = scale;
+    if (need > 0) {
+        a.stat = static_cast<float *>(workspace);
+        a.list = reinterpret_cast<uint64_t *>(a.stat + 4 * n * parts);
+    }
+    return qk::launch_token_logprobs(a, x_dtype == QK_F16, each, static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

@@ -23,7 +23,8 @@ FORMATS = {"q4_0": QK_Q4_0, "q4_1": QK_Q4_1, "q8_0": QK_Q8_0, "q5_0": QK_Q5_0, "
 SYMBOLS = ("qk_block_bytes", "qk_row_bytes", "qk_status_string", "qk_version",
            "qk_dequantize", "qk_mul_mat_vec", "qk_mul_mat_vec_x8", "qk_mul_mat_vec_batched",
            "qk_mul_mat_vec_id", "qk_mul_mat", "qk_mul_mat_vec_x8q", "qk_rms_norm", "qk_kv_store",
-           "qk_attn_decode", "qk_attn_decode_workspace", "qk_moe_route")
+           "qk_attn_decode", "qk_attn_decode_workspace", "qk_moe_route", "qk_kv_copy", "qk_kv_fork", "qk_kv_compact",
+           "qk_kv_pages_workspace", "qk_token_logprobs", "qk_token_logprobs_workspace")
 QK_MAX_BATCH = 16
 X8_BLOCK_BYTES = 36  # an 8-bit activation block: fp32 scale, 32 int8 codes
 
@@ -101,6 +102,20 @@ def load():
     lib.qk_moe_route.argtypes = [vp, i64, i64, i64, i64, ci, vp, i64, i64, i64, ci, ctypes.c_float,
                                  vp, i64, vp, i64, vp]
     lib.qk_moe_route.restype = ci
+    lib.qk_kv_copy.argtypes = [cache, vp, vp, i64, vp]
+    lib.qk_kv_copy.restype = ci
+    lib.qk_kv_fork.argtypes = [vp, i64, vp, i64, i64, vp, vp, i64, i64, i64, i64, vp, i64, vp, vp, vp, vp,
+                               ctypes.c_size_t, vp]
+    lib.qk_kv_fork.restype = ci
+    lib.qk_kv_compact.argtypes = [vp, i64, vp, i64, i64, i64, i64, vp, i64, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.qk_kv_compact.restype = ci
+    lib.qk_kv_pages_workspace.argtypes = [i64, i64]
+    lib.qk_kv_pages_workspace.restype = ctypes.c_size_t
+    lib.qk_token_logprobs.argtypes = [ci, vp, i64, i64, i64, ctypes.c_float, vp, i64, i64, vp, i64, vp, i64, vp, i64,
+                                      vp, i64, vp, ctypes.c_size_t, vp]
+    lib.qk_token_logprobs.restype = ci
+    lib.qk_token_logprobs_workspace.argtypes = [i64, i64, i64]
+    lib.qk_token_logprobs_workspace.restype = ctypes.c_size_t
     _lib = lib
     return lib
 
@@ -210,6 +225,40 @@ def qk_moe_route(logits_ptr, ldx, n_tokens, n_experts, n_used, score, bias_ptr, 
                  renorm, scale, ids_ptr, ld_ids, weights_ptr, ldw, stream=0):
     return load().qk_moe_route(logits_ptr, ldx, n_tokens, n_experts, n_used, score, bias_ptr, n_groups,
                                topk_groups, group_top, renorm, scale, ids_ptr, ld_ids, weights_ptr, ldw, stream)
+
+
+def qk_kv_copy(cache, src_ptr, dst_ptr, n, stream=0):
+    """cache: a KVCacheDesc or None."""
+    return load().qk_kv_copy(cache, src_ptr, dst_ptr, n, stream)
+
+
+def qk_kv_fork(table_ptr, ld_table, lens_ptr, n_rows, in_pages, parent_ptr, new_lens_ptr, n_new, out_pages, page_size,
+               n_pages, out_ptr, ld_out, src_ptr, dst_ptr, missing_ptr, workspace_ptr, workspace_bytes, stream=0):
+    return load().qk_kv_fork(table_ptr, ld_table, lens_ptr, n_rows, in_pages, parent_ptr, new_lens_ptr, n_new,
+                             out_pages, page_size, n_pages, out_ptr, ld_out, src_ptr, dst_ptr, missing_ptr,
+                             workspace_ptr, workspace_bytes, stream)
+
+
+def qk_kv_compact(table_ptr, ld_table, lens_ptr, n_rows, max_pages, page_size, n_pages, out_ptr, ld_out, src_ptr,
+                  dst_ptr, live_ptr, workspace_ptr, workspace_bytes, stream=0):
+    return load().qk_kv_compact(table_ptr, ld_table, lens_ptr, n_rows, max_pages, page_size, n_pages, out_ptr, ld_out,
+                                src_ptr, dst_ptr, live_ptr, workspace_ptr, workspace_bytes, stream)
+
+
+def qk_kv_pages_workspace(n_rows, n_pages):
+    return load().qk_kv_pages_workspace(n_rows, n_pages)
+
+
+def qk_token_logprobs(x_dtype, logits_ptr, ldx, n, vocab, scale, ids_ptr, ld_ids, n_ids, logprobs_ptr, ld_logprobs,
+                      entropy_ptr, top, best_ids_ptr, ld_best_ids, best_ptr, ld_best, workspace_ptr, workspace_bytes,
+                      stream=0):
+    return load().qk_token_logprobs(x_dtype, logits_ptr, ldx, n, vocab, scale, ids_ptr, ld_ids, n_ids, logprobs_ptr,
+                                    ld_logprobs, entropy_ptr, top, best_ids_ptr, ld_best_ids, best_ptr, ld_best,
+                                    workspace_ptr, workspace_bytes, stream)
+
+
+def qk_token_logprobs_workspace(n, vocab, top=0):
+    return load().qk_token_logprobs_workspace(n, vocab, top)
 
 
 # ---------------------------------------------------------------------------
@@ -765,3 +814,172 @@ def moe_route(logits, n_used, score="softmax", bias=None, n_groups=1, topk_group
                              _stream_of(logits))
     _check(st, "qk_moe_route")
     return ids, weights
+
+
+# Sequences that share pages, and what their answers are chosen by.
+
+def _scratch(workspace, need, device):
+    """The caller's workspace, or one of its own where one is needed."""
+    import torch
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    if not isinstance(workspace, torch.Tensor) or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous uint8 tensor")
+    return workspace
+
+
+def _ptr_bytes(t):
+    return (t.data_ptr(), t.numel()) if t is not None else (None, 0)
+
+
+def kv_copy(cache, src, dst, stream=None):
+    """Copy whole pages of a paged cache (keys, values, scales): page dst[i] =
+    page src[i], int32 (n,), as kv_fork and kv_compact list them.  A pair with
+    an id outside the pool (-1) is left out.  No page may be written twice, nor
+    written by one pair and read by another."""
+    _int32_check(src, "src", 1)
+    _int32_check(dst, "dst", 1)
+    if src.shape != dst.shape:
+        raise ValueError(f"src has {src.shape[0]} pages, dst {dst.shape[0]}")
+    _on_device(cache.k, src, dst)
+    st = load().qk_kv_copy(cache.desc, src.data_ptr(), dst.data_ptr(), src.shape[0], _stream_of(cache.k, stream))
+    _check(st, "qk_kv_copy")
+
+
+def kv_pages_workspace(n_rows, n_pages, device="cuda"):
+    """Scratch for kv_fork and kv_compact calls of up to these sizes: a uint8
+    tensor.  One tensor serves one stream at a time."""
+    import torch
+    need = qk_kv_pages_workspace(n_rows, n_pages)
+    if not need:
+        raise ValueError(f"bad sizes: {n_rows} rows, {n_pages} pages")
+    return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def _table_check(table, lens):
+    _int32_check(table, "table", 2)
+    _int32_check(lens, "lens", 1)
+    if lens.shape[0] != table.shape[0]:
+        raise ValueError(f"table has {table.shape[0]} rows, lens {lens.shape[0]}")
+
+
+def _pages_check(page_size, n_pages):
+    if not 1 <= page_size <= 1 << 20 or not 1 <= n_pages < 1 << 31:
+        raise ValueError(f"page_size {page_size}, n_pages {n_pages}")
+
+
+def kv_fork(table, lens, new_lens, page_size, n_pages, parent=None, out=None, workspace=None, stream=None):
+    """The page table of the next step: row i takes over the tokens of row
+    parent[i] (row i itself without parent; an empty sequence where parent[i]
+    is no row), at most new_lens[i] of them, and gets pages for new_lens[i]
+    tokens.  table int32 (n_rows, pages), lens int32 (n_rows,); new_lens and
+    parent int32 (n_new,).  Returns (table, src, dst, missing): src and dst
+    int32 (n_new,) list the pages that kv_copy must copy before rows write on in
+    pages that they share (-1: none); missing int32 (1,) counts the pages that
+    could not be had (their entries are -1).  out: (n_new, any number of
+    pages), or table itself to change it in place, without parent."""
+    import torch
+    if stream is not None:
+        return _on_stream(stream, table, kv_fork, table, lens, new_lens, page_size, n_pages, parent, out, workspace)
+    _table_check(table, lens)
+    _int32_check(new_lens, "new_lens", 1)
+    _pages_check(page_size, n_pages)
+    n = new_lens.shape[0]
+    if parent is not None:
+        _int32_check(parent, "parent", 1)
+        if parent.shape[0] != n:
+            raise ValueError(f"parent has {parent.shape[0]} rows, new_lens {n}")
+    if out is None:
+        out = table.new_empty((n, table.shape[1]))
+    else:
+        _int32_check(out, "out", 2)
+        if out.shape[0] != n:
+            raise ValueError(f"out has {out.shape[0]} rows, new_lens {n}")
+    # (one allocation for the three small outputs)
+    small = table.new_empty(2 * n + 1)
+    src, dst, missing = small[:n], small[n:2 * n], small[2 * n:]
+    _on_device(table, lens, new_lens, parent, out, workspace)
+    work, size = _ptr_bytes(_scratch(workspace, 0 if workspace is not None else qk_kv_pages_workspace(n, n_pages), table.device))
+    st = load().qk_kv_fork(table.data_ptr(), table.stride(0), lens.data_ptr(), table.shape[0], table.shape[1],
+                           parent.data_ptr() if parent is not None else None, new_lens.data_ptr(), n, out.shape[1],
+                           page_size, n_pages, out.data_ptr(), out.stride(0), src.data_ptr(), dst.data_ptr(),
+                           missing.data_ptr(), work, size, _stream_of(table))
+    _check(st, "qk_kv_fork")
+    return out, src, dst, missing
+
+
+def kv_compact(table, lens, page_size, n_pages, out=None, workspace=None, stream=None):
+    """Pack the pages that the rows of table int32 (n_rows, pages) hold for lens
+    int32 (n_rows,) tokens into the first pages of the pool.  Returns (table,
+    src, dst, live): src and dst int32 (n_pages // 2,) are the moves for
+    kv_copy (-1 behind the last), live int32 (1,) the number of pages held.
+    out may be table itself."""
+    import torch
+    if stream is not None:
+        return _on_stream(stream, table, kv_compact, table, lens, page_size, n_pages, out, workspace)
+    _table_check(table, lens)
+    _pages_check(page_size, n_pages)
+    if out is None:
+        out = table.new_empty(table.shape)
+    else:
+        _int32_check(out, "out", 2)
+        if out.shape != table.shape:
+            raise ValueError(f"out must be {tuple(table.shape)}, got {tuple(out.shape)}")
+    n = n_pages // 2
+    src, dst, live = table.new_empty(n), table.new_empty(n), table.new_empty(1)
+    _on_device(table, lens, out, workspace)
+    work, size = _ptr_bytes(_scratch(workspace, 0 if workspace is not None else qk_kv_pages_workspace(table.shape[0], n_pages),
+                                     table.device))
+    st = load().qk_kv_compact(table.data_ptr(), table.stride(0), lens.data_ptr(), table.shape[0], table.shape[1],
+                              page_size, n_pages, out.data_ptr(), out.stride(0), src.data_ptr(), dst.data_ptr(),
+                              live.data_ptr(), work, size, _stream_of(table))
+    _check(st, "qk_kv_compact")
+    return out, src, dst, live
+
+
+def token_logprobs_workspace(n, vocab, top=0, device="cuda"):
+    """Scratch for token_logprobs calls of up to these sizes: a uint8 tensor, or
+    None where none is needed.  One tensor serves one stream at a time."""
+    import torch
+    need = qk_token_logprobs_workspace(n, vocab, top)
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+
+
+def token_logprobs(logits, ids=None, top=0, scale=1.0, workspace=None, stream=None):
+    """Log probabilities under softmax(scale * logits) of rows of logits (n,
+    vocab), fp32 or fp16.  ids int32 (n,) or (n, m): the tokens asked for.
+    Returns (logprobs fp32 as ids, or None; entropy fp32 (n,); best_ids int32
+    (n, top) and their log probabilities fp32 (n, top), the largest first and
+    of equal logits the lowest index, or None and None with top 0)."""
+    import torch
+    if stream is not None:
+        return _on_stream(stream, logits, token_logprobs, logits, ids, top, scale, workspace)
+    dtype = logits.dtype if isinstance(logits, torch.Tensor) else None
+    if dtype is not torch.float32 and dtype is not torch.float16:
+        raise TypeError("logits must be a float32 or float16 tensor")
+    if logits.dim() != 2 or logits.shape[1] < 1 or (not logits.is_contiguous() and logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError(f"logits must be (n, vocab) with contiguous rows, got {tuple(logits.shape)}")
+    n, vocab = logits.shape
+    if not 0 <= top <= min(64, vocab):
+        raise ValueError(f"top must be 0..{min(64, vocab)}, got {top}")
+    if not 0.0 < scale < float("inf"):
+        raise ValueError(f"scale must be positive and finite, got {scale}")
+    lp, ip, ld_ids, m = None, None, 0, 0
+    if ids is not None:
+        _int32_check(ids, "ids", ids.dim() if isinstance(ids, torch.Tensor) and ids.dim() in (1, 2) else 2)
+        if ids.shape[0] != n:
+            raise ValueError(f"ids has {ids.shape[0]} rows, logits {n}")
+        m = ids.shape[1] if ids.dim() == 2 else 1
+        lp, ip, ld_ids = logits.new_empty(ids.shape, dtype=torch.float32), ids.data_ptr(), ids.stride(0)
+    entropy = logits.new_empty(n, dtype=torch.float32)
+    best_ids = logits.new_empty((n, top), dtype=torch.int32) if top else None
+    best = logits.new_empty((n, top), dtype=torch.float32) if top else None
+    _on_device(logits, ids, workspace)
+    work, size = _ptr_bytes(_scratch(workspace, 0 if workspace is not None else qk_token_logprobs_workspace(n, vocab, top),
+                                     logits.device))
+    st = load().qk_token_logprobs(QK_F32 if dtype is torch.float32 else QK_F16, logits.data_ptr(), logits.stride(0), n,
+                                  vocab, scale, ip, ld_ids, m, lp.data_ptr() if lp is not None else None, m,
+                                  entropy.data_ptr(), top, best_ids.data_ptr() if top else None, top,
+                                  best.data_ptr() if top else None, top, work, size, _stream_of(logits))
+    _check(st, "qk_token_logprobs")
+    return lp, entropy, best_ids, best

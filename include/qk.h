@@ -1,7 +1,9 @@
 /*
  * qk.h - C ABI of libqk: ggml block-quantized dequantize, GEMV and GEMM on
  * AMD gfx950 (MI355X), and what a decode step has between them: RMS norm,
- * paged key-value cache and its attention, routing to experts.
+ * paged key-value cache and its attention, routing to experts; with what many
+ * answers to one prompt take besides: pages that sequences share, attention
+ * that reads them once, and log probabilities to choose by.
  *
  * Block formats (32 weights per block, little-endian binary16 fields, blocks
  * packed back to back, a matrix stored row after row with k/32 blocks per row
@@ -391,6 +393,92 @@ int qk_kv_store(const qk_kv_cache *cache, const float *k, int64_t k_tok, int64_t
                 const int32_t *seq, const int32_t *pos, void *stream);
 
 /*
+ * Pages that sequences share.  A page table (see qk_kv_cache) is all the
+ * state: row i holds the pages that its lens[i] tokens lie in, a page may be
+ * held by several rows, and a page that no row holds is free.  A sequence is
+ * dropped by giving its row no tokens; there are no counts to keep.  The
+ * calls work on tables alone, so one plan serves the caches of all layers: each
+ * is then brought into line by qk_kv_copy with the lists of pages that the
+ * plan gives.  Ids outside the pool are kept as they are and hold nothing;
+ * lengths are taken as 0 below 0 and no more than a row has room for.
+ */
+
+/*
+ * qk_kv_copy - copy whole pages of a cache: keys, values, and the scales of
+ * 8 bits.
+ *
+ *   page dst[i] = page src[i]     for i < n
+ *
+ * A pair with an id outside the pool is left out, as the plans' lists have -1
+ * where there is nothing to copy.  No page may be written twice, nor written
+ * and read by different pairs, in one call.
+ *
+ *   src, dst   device int32[n], n >= 0 (0 is a no-op)
+ * Errors as qk_kv_store where rows of the pools overlap.
+ */
+int qk_kv_copy(const qk_kv_cache *cache, const int32_t *src, const int32_t *dst, int64_t n, void *stream);
+
+/*
+ * qk_kv_fork - the page table of the next step: sequences forked, put in
+ * another order, dropped, cut short, and given room for new tokens.
+ *
+ *   row i of out takes the first min(L, N) tokens of row parent[i] of table,
+ *   with L = lens[parent[i]] and N = new_lens[i], and has pages for N tokens
+ *
+ * Rows of one parent share its pages.  Where row i is to be written on inside
+ * a page that it shares (N > L, L not a multiple of page_size, and the page held
+ * elsewhere in out too), it gets a page of its own for it, and src[i], dst[i] are
+ * the two pages for qk_kv_copy; otherwise both are -1.  Requests for pages, row by
+ * row and by position, take the free pages in ascending order; a page is free
+ * if out takes it over nowhere.  Where pages run out the entry is -1 (src[i] and
+ * dst[i] too) and *missing counts it: table is as it was, unless it was
+ * replaced in place.  Entries past a row's pages are -1.
+ *
+ *   table      device int32, n_rows rows of in_pages ids, stride ld_table
+ *   lens       device int32[n_rows]
+ *   parent     device int32[n_new], or NULL: row i from row i.  A parent
+ *              outside 0..n_rows-1 is an empty sequence
+ *   new_lens   device int32[n_new]; <= 0: the row holds nothing
+ *   out        device int32, n_new rows of out_pages ids, stride ld_out.  May
+ *              be table itself with parent == NULL and the same sizes
+ *   src, dst   device int32[n_new]
+ *   missing    device int32: pages that could not be had
+ *   n_pages    pages of the pool, 1..INT32_MAX
+ *   page_size  1..2^20
+ *   workspace  16-byte aligned device memory of the bytes that
+ *              qk_kv_pages_workspace gives for n_new rows and n_pages or more;
+ *              it need not be cleared
+ * in_pages, out_pages 0..2^30; n_new * out_pages and n_new * in_pages <= INT32_MAX;
+ * strides are ignored for a single row.
+ */
+int qk_kv_fork(const int32_t *table, int64_t ld_table, const int32_t *lens, int64_t n_rows, int64_t in_pages,
+               const int32_t *parent, const int32_t *new_lens, int64_t n_new, int64_t out_pages,
+               int64_t page_size, int64_t n_pages, int32_t *out, int64_t ld_out, int32_t *src, int32_t *dst,
+               int32_t *missing, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * qk_kv_compact - pack the pages that rows hold together at the pool's
+ * beginning.
+ *
+ *   n = number of pages held; those from page n on move, in ascending order, to the
+ *   free pages below n, in ascending order
+ *
+ * out is table with the new ids (-1 past each row's pages); src and dst are
+ * the moves for qk_kv_copy, n_pages / 2 entries (the most there can be), -1
+ * behind the last; *live is n.
+ *
+ *   table, lens, out, workspace   as qk_kv_fork; out may be table itself
+ *   src, dst                      device int32[n_pages / 2]
+ */
+int qk_kv_compact(const int32_t *table, int64_t ld_table, const int32_t *lens, int64_t n_rows, int64_t max_pages,
+                  int64_t page_size, int64_t n_pages, int32_t *out, int64_t ld_out, int32_t *src, int32_t *dst,
+                  int32_t *live, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that serve qk_kv_fork and qk_kv_compact with up to n_rows
+ * rows and n_pages pages; 0 on a bad argument. */
+size_t qk_kv_pages_workspace(int64_t n_rows, int64_t n_pages);
+
+/*
  * qk_attn_decode - attention of one new token per sequence over a paged cache.
  *
  *   z_t = scale * q . K_t    for the tokens t < lens[s] that the query sees
@@ -478,6 +566,47 @@ int qk_moe_route(const float *logits, int64_t ldx, int64_t n_tokens, int64_t n_e
                  int64_t n_used, int score, const float *bias, int64_t n_groups,
                  int64_t topk_groups, int64_t group_top, int renorm, float scale,
                  int32_t *ids, int64_t ld_ids, float *weights, int64_t ldw, void *stream);
+
+/*
+ * qk_token_logprobs - log probabilities of given tokens, the entropy and the
+ * best alternatives of rows of logits (a vocabulary's, from the last product).
+ *
+ *   logprobs[r][i] = z_id - ln S       id = ids[r][i]
+ *   entropy[r]     = -sum_j p_j ln p_j
+ *   best_ids[r][i] = the token with the i-th largest logit, i < top
+ *   best[r][i]     = its log probability
+ *   with z_j = scale * x_rj, S = sum_j exp(z_j), p_j = exp(z_j) / S
+ *
+ * Equal logits: the lowest index first.  The sums are over the row's largest
+ * logit, which is left out of them and counted, so that log probabilities near 0
+ * and small entropies keep their digits.  Logits of -infinity have probability 0;
+ * a row of nothing else gives -infinity and entropy 0.  A row with a NaN or a
+ * +infinite logit gives NaN throughout (its best_ids as ever, NaN last).  An
+ * id outside the vocabulary gives NaN.
+ *
+ *   x_dtype    QK_F32 or QK_F16
+ *   logits     n rows of vocab elements, stride ldx >= vocab
+ *   vocab      1..2^30; n >= 0 (0 is a no-op)
+ *   scale      > 0 and finite: 1 / temperature
+ *   ids        device int32, n rows of n_ids tokens, stride ld_ids; NULL with n_ids 0
+ *   n_ids      0..2^20
+ *   logprobs   fp32, stride ld_logprobs >= n_ids; NULL with n_ids 0
+ *   entropy    fp32[n], or NULL to leave it out
+ *   top        0..64, at most vocab
+ *   best_ids, best   int32 and fp32, strides >= top; NULL with top 0
+ *   workspace  16-byte aligned device memory of the bytes that
+ *              qk_token_logprobs_workspace gives for these sizes or larger
+ *              ones (NULL if 0); it need not be cleared
+ * Strides are ignored if n == 1.
+ */
+int qk_token_logprobs(int x_dtype, const void *logits, int64_t ldx, int64_t n, int64_t vocab, float scale,
+                      const int32_t *ids, int64_t ld_ids, int64_t n_ids, float *logprobs, int64_t ld_logprobs,
+                      float *entropy, int64_t top, int32_t *best_ids, int64_t ld_best_ids, float *best, int64_t ld_best,
+                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that serve qk_token_logprobs with up to n rows, vocab
+ * logits and top alternatives; 0 where none is needed, and on a bad argument. */
+size_t qk_token_logprobs_workspace(int64_t n, int64_t vocab, int64_t top);
 
 #ifdef __cplusplus
 }
