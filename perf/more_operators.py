@@ -265,7 +265,7 @@ def prepare(c, seed):
         if op in ("copy", "attn"):
             s["cache"] = qk.KVCache(s["kc"], s["vc"], s["ks"], s["vs"])
         if op == "attn":
-            s["scratch"] = qk.attn_decode_shared_workspace(s["cache"], c["seqs"], c["q_heads"], c["groups"],
+            s["scratch"] = qk.attn_decode_shared_workspace(s["cache"], c["seqs"], c["q_heads"],
                                                            c["shared"] + c["tail"], c["shared"], c["tail"])
         elif op == "fork":
             s["scratch"] = qk.kv_pages_workspace(c["rows"], s["pages"])
