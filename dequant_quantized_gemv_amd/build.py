@@ -22,7 +22,7 @@ SOURCES = ["api.hip", "dequant.hip", "gemv.hip", "gemv_n1.hip", "gemv_n2.hip", "
            "gemv_n56.hip", "gemv_n78.hip", "gemv_id.hip", "gemv_x8_n1.hip", "gemv_x8_n24.hip",
            "gemv_x8_n58.hip", "gemv_x8q_n1.hip", "gemv_x8q_n23.hip", "gemv_x8q_mfma.hip",
            "gemm.hip", "norm.hip", "kv_store.hip", "attn_f16.hip", "attn_i8.hip", "route.hip",
-           "kv_pages.hip", "logprobs.hip"]
+           "attn_shared_f16.hip", "attn_shared_i8.hip", "kv_pages.hip", "logprobs.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -43,6 +43,8 @@ SOURCE_FLAGS = {
     "gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "attn_f16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "attn_i8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "attn_shared_f16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "attn_shared_i8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }
 
 

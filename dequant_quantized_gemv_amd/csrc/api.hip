@@ -225,6 +225,89 @@ size_t attn_workspace_bound(const qk_kv_cache &c, const qk::AttnArgs &a) {
     return 4 * (size_t)parts * a.n_heads * (size_t)qk::attn_part_floats((int)c.head_dim);
 }
 
+// The cache and the operands of an attention; whether sub-tiles of 16 tokens
+// lie in one page, their rows within 32-bit offsets.
+bool attn_fill(const qk_kv_cache &c, qk::AttnArgs &a, const float *q, int64_t q_seq, int64_t q_head, const int32_t *table,
+               int64_t ld_table, const int32_t *lens, float scale, int y_dtype, void *y, int64_t y_seq, int64_t y_head,
+               void *workspace) {
+    const bool i8 = c.type == QK_KV_I8;
+    const int64_t es = i8 ? 1 : 2;
+    a.k = static_cast<const uint8_t *>(c.k);
+    a.v = static_cast<const uint8_t *>(c.v);
+    a.ks = c.k_scale;
+    a.vs = c.v_scale;
+    a.q = q;
+    a.table = table;
+    a.lens = lens;
+    a.y = y;
+    a.part = static_cast<float *>(workspace);
+    a.page_stride = c.page_stride * es;
+    a.head_stride = c.head_stride * es;
+    a.slot_stride = c.slot_stride * es;
+    a.sc_page = c.scale_page_stride;
+    a.sc_head = c.scale_head_stride;
+    a.sc_slot = c.scale_slot_stride;
+    a.q_seq = q_seq;
+    a.q_head = q_head;
+    a.y_seq = y_seq;
+    a.y_head = y_head;
+    a.ld_table = ld_table;
+    a.qscale = (float)((double)scale * 1.4426950408889634);
+    a.out_f16 = y_dtype == QK_F16;
+    return c.page_size % 16 == 0 && a.slot_stride < (int64_t(1) << 26) && (!i8 || c.scale_slot_stride == 1);
+}
+
+// Sizes and splits of an attention with shared first tokens.  Rows of 32 where
+// the groups have no more than that many query rows on average, else of 128.
+int shared_plan(const qk_kv_cache &c, int64_t n_seqs, int64_t n_q_heads, int64_t n_groups, int64_t max_len,
+                int64_t max_shared, int64_t max_own, qk::SharedArgs &a) {
+    if (n_groups < 0 || n_groups > kMaxDim || max_shared < 0 || max_own < 1 || max_len < 1 || max_len > (int64_t(1) << 30) ||
+        max_shared > max_len || max_own > max_len)
+        return QK_ERR_INVALID_ARG;
+    // (a sequence's own tokens begin anywhere in a 32-token tile)
+    const int st = attn_plan(c, n_seqs, n_q_heads, std::min<int64_t>(max_own + qk::kAttnTile - 1, int64_t(1) << 30), 0, 0, a);
+    if (st != QK_OK) return st;
+    a.max_len = (int)max_len;
+    a.n_groups = (int)n_groups;
+    a.max_shared = (int)max_shared;
+    a.max_own = (int)max_own;
+    if (n_seqs == 0) return QK_OK;
+    a.prefix_chunks = 0;
+    a.prefix_tiles = 1;
+    if (n_groups > 0 && max_shared > 0) {
+        const int64_t groups = std::min(n_groups, n_seqs);
+        const int64_t each = (n_seqs * a.group + groups - 1) / groups;   // query rows of a group
+        a.wide = each > 32;
+        const int64_t rows = qk::prefix_rows(a.wide), tokens = qk::prefix_tokens(a.wide);
+        // row tiles at most, and about as many as there will be
+        a.row_tiles = (int)(n_seqs * a.group / rows + groups);
+        const int64_t about = groups * ((each + rows - 1) / rows);
+        const int64_t tiles = (max_shared + tokens - 1) / tokens, target = attn_target(c);
+        a.prefix_tiles = (int)std::max<int64_t>(1, std::min(tiles, (tiles * a.n_kv * about + target - 1) / target));
+        a.prefix_chunks = (int)((tiles + a.prefix_tiles - 1) / a.prefix_tiles);
+    }
+    if ((int64_t)a.n_kv * a.prefix_chunks > (1 << 22)) return QK_ERR_INVALID_ARG;
+    a.slots = a.prefix_chunks + a.nchunks;
+    return QK_OK;
+}
+
+size_t shared_workspace(const qk_kv_cache &c, const qk::SharedArgs &a) {
+    return 4 * (size_t)a.n_seqs * a.n_heads * a.slots * (size_t)qk::attn_part_floats((int)c.head_dim);
+}
+
+// The most that shared_workspace() asks for over calls of up to these sizes and
+// any groups.  Chunks of shared tokens: a tile at least, and no more than give
+// target workgroups with the group's row tiles (128 rows at most) and one more.
+// Chunks of own tokens: as in attn_workspace_bound, but one at least.
+size_t shared_workspace_bound(const qk_kv_cache &c, const qk::SharedArgs &a) {
+    const int64_t target = attn_target(c), seqs = a.n_seqs, heads = a.n_heads;
+    int64_t parts = 0;
+    if (a.max_shared > 0) parts = std::min(seqs * heads * ((a.max_shared + 63) / 64), seqs * heads + target * qk::prefix_rows(1));
+    const int64_t tiles = ((int64_t)a.max_own + 2 * qk::kAttnTile - 2) / qk::kAttnTile, row = (int64_t)a.n_kv * a.head_tiles;
+    parts += heads * std::min(seqs * ((tiles + qk::kAttnWaves - 1) / qk::kAttnWaves), target / row + seqs);
+    return 4 * (size_t)parts * (size_t)qk::attn_part_floats((int)c.head_dim);
+}
+
 }  // namespace
 
 extern "C" {
@@ -535,34 +618,63 @@ int qk_attn_decode(const qk_kv_cache *cache, const float *q, int64_t q_seq, int6
     for (const Range &r : cache_ranges(c))
         if (overlaps(r.p, r.n, y, yb) || overlaps(r.p, r.n, workspace, need)) return QK_ERR_INVALID_ARG;
     const bool i8 = c.type == QK_KV_I8;
-    const int64_t es = i8 ? 1 : 2;
-    a.k = static_cast<const uint8_t *>(c.k);
-    a.v = static_cast<const uint8_t *>(c.v);
-    a.ks = c.k_scale;
-    a.vs = c.v_scale;
-    a.q = q;
-    a.table = table;
-    a.lens = lens;
-    a.y = y;
-    a.part = static_cast<float *>(workspace);
-    a.page_stride = c.page_stride * es;
-    a.head_stride = c.head_stride * es;
-    a.slot_stride = c.slot_stride * es;
-    a.sc_page = c.scale_page_stride;
-    a.sc_head = c.scale_head_stride;
-    a.sc_slot = c.scale_slot_stride;
-    a.q_seq = q_seq;
-    a.q_head = q_head;
-    a.y_seq = y_seq;
-    a.y_head = y_head;
-    a.ld_table = ld_table;
-    a.qscale = (float)((double)scale * 1.4426950408889634);
-    a.out_f16 = y_dtype == QK_F16;
-    // sub-tiles of 16 tokens in one page, their rows within 32-bit offsets
-    const bool tiled = c.page_size % 16 == 0 && a.slot_stride < (int64_t(1) << 26) && (!i8 || c.scale_slot_stride == 1);
+    const bool tiled = attn_fill(c, a, q, q_seq, q_head, table, ld_table, lens, scale, y_dtype, y, y_seq, y_head, workspace);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     return i8 ? qk::attn_decode_run<true>(a, (int)c.head_dim, tiled, s)
               : qk::attn_decode_run<false>(a, (int)c.head_dim, tiled, s);
+}
+
+size_t qk_attn_decode_shared_workspace(const qk_kv_cache *cache, int64_t n_seqs, int64_t n_q_heads, int64_t max_len,
+                                       int64_t max_shared, int64_t max_own) {
+    if (check_cache(cache) != QK_OK) return 0;
+    qk::SharedArgs a{};
+    if (shared_plan(*cache, n_seqs, n_q_heads, 1, max_len, max_shared, max_own, a) != QK_OK || n_seqs == 0) return 0;
+    return shared_workspace_bound(*cache, a);
+}
+
+int qk_attn_decode_shared(const qk_kv_cache *cache, const float *q, int64_t q_seq, int64_t q_head,
+                          int64_t n_seqs, int64_t n_q_heads, const int32_t *table, int64_t ld_table,
+                          const int32_t *lens, int64_t max_len, const int32_t *starts, const int32_t *shared,
+                          int64_t n_groups, int64_t max_shared, int64_t max_own, float scale,
+                          int y_dtype, void *y, int64_t y_seq, int64_t y_head,
+                          void *workspace, size_t workspace_bytes, void *stream) {
+    if (y_dtype != QK_F32 && y_dtype != QK_F16) return QK_ERR_UNSUPPORTED;
+    int st = check_cache(cache);
+    if (st != QK_OK) return st;
+    const qk_kv_cache &c = *cache;
+    qk::SharedArgs a{};
+    st = shared_plan(c, n_seqs, n_q_heads, n_groups, max_len, max_shared, max_own, a);
+    if (st != QK_OK) return st;
+    if (n_seqs == 0) return QK_OK;
+    if (q == nullptr || y == nullptr || table == nullptr || lens == nullptr || workspace == nullptr ||
+        (n_groups > 0 && (starts == nullptr || shared == nullptr)))
+        return QK_ERR_INVALID_ARG;
+    const int64_t pages = (max_len + c.page_size - 1) / c.page_size;
+    if (n_seqs == 1) ld_table = pages;
+    if (ld_table < pages || !stride_ok(ld_table)) return QK_ERR_INVALID_ARG;
+    if (!stride_ok(q_seq) || !stride_ok(q_head) || !stride_ok(y_seq) || !stride_ok(y_head)) return QK_ERR_INVALID_ARG;
+    if (!rows_disjoint(c.head_dim, {{n_seqs, y_seq}, {n_q_heads, y_head}})) return QK_ERR_INVALID_ARG;
+    const size_t ye = y_dtype == QK_F32 ? 4 : 2;
+    if (((uintptr_t)q | (uintptr_t)table | (uintptr_t)lens | (uintptr_t)starts | (uintptr_t)shared) % 4 != 0 ||
+        (uintptr_t)y % ye != 0 || (uintptr_t)workspace % 16 != 0)
+        return QK_ERR_ALIGNMENT;
+    const size_t need = shared_workspace(c, a);
+    if (workspace_bytes < need) return QK_ERR_INVALID_ARG;
+    const size_t qb = 4 * (size_t)(c.head_dim + (n_seqs - 1) * q_seq + (n_q_heads - 1) * q_head);
+    const size_t yb = ye * (size_t)(c.head_dim + (n_seqs - 1) * y_seq + (n_q_heads - 1) * y_head);
+    const Range in[] = {{q, qb}, {table, 4 * span_bytes(n_seqs, ld_table, pages, 1)}, {lens, 4 * (size_t)n_seqs},
+                        {starts, n_groups > 0 ? 4 * (size_t)(n_groups + 1) : 0}, {shared, 4 * (size_t)n_groups}};
+    if (overlaps(y, yb, workspace, need)) return QK_ERR_INVALID_ARG;
+    for (const Range &r : in)
+        if (overlaps(r.p, r.n, y, yb) || overlaps(r.p, r.n, workspace, need)) return QK_ERR_INVALID_ARG;
+    for (const Range &r : cache_ranges(c))
+        if (overlaps(r.p, r.n, y, yb) || overlaps(r.p, r.n, workspace, need)) return QK_ERR_INVALID_ARG;
+    a.starts = starts;
+    a.shared = shared;
+    const bool tiled = attn_fill(c, a, q, q_seq, q_head, table, ld_table, lens, scale, y_dtype, y, y_seq, y_head, workspace);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    return c.type == QK_KV_I8 ? qk::attn_shared_run<true>(a, (int)c.head_dim, tiled, s)
+                              : qk::attn_shared_run<false>(a, (int)c.head_dim, tiled, s);
 }
 
 int qk_moe_route(const float *logits, int64_t ldx, int64_t n_tokens, int64_t n_experts, int64_t n_used,

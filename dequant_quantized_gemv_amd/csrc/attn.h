@@ -32,6 +32,18 @@ struct AttnArgs {
     int out_f16;
 };
 
+// The attention of sequences of which groups share their first tokens: group g
+// is sequences starts[g] .. starts[g + 1] - 1, shared[g] tokens in the pages of
+// its first sequence.  A (sequence, head) has `slots` partial results, first
+// those of the shared tokens' chunks, then those of its own (nchunks).
+struct SharedArgs : AttnArgs {
+    const int32_t *starts, *shared;
+    int n_groups, max_shared, max_own;
+    int prefix_tiles, prefix_chunks, slots;   // tiles of a chunk of shared tokens; chunks
+    int row_tiles, wide;                      // tiles of query rows; 128 rows each, else 32
+    int seq0, tile0;                          // first sequence, first row tile of this launch
+};
+
 // One partial result: the running maximum and sum, then head_dim outputs.
 constexpr int64_t attn_part_floats(int head_dim) { return head_dim + 4; }
 
@@ -55,6 +67,16 @@ __host__ __device__ inline AttnSpan attn_span(int len, int window, int sinks) {
     return s;
 }
 
+// A sequence's own tokens behind `shared`.
+__host__ __device__ inline AttnSpan own_span(int len, int shared) {
+    const int start = shared & ~(kAttnTile - 1);
+    return AttnSpan{len, shared, start, 0, (len - start + kAttnTile - 1) / kAttnTile};
+}
+
+// Query rows of a tile and tokens of a tile of the shared tokens' kernel.
+constexpr int prefix_rows(int wide) { return wide ? 128 : 32; }
+constexpr int prefix_tokens(int wide) { return wide ? 64 : 128; }
+
 struct StoreArgs {
     uint8_t *kc, *vc;
     float *ks, *vs;
@@ -69,5 +91,6 @@ struct StoreArgs {
 };
 
 template <bool I8> int attn_decode_run(const AttnArgs &a, int head_dim, bool tiled, hipStream_t stream);
+template <bool I8> int attn_shared_run(const SharedArgs &a, int head_dim, bool tiled, hipStream_t stream);
 
 }  // namespace qk

@@ -39,6 +39,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "attn.h"
 #include "qk_common.h"
@@ -133,12 +134,34 @@ __device__ __forceinline__ Bytes<N> load_bytes(const uint8_t *p) {
     return r;
 }
 
+// The tokens that sequence seq of len tokens shares with its group (0 without a
+// group), found by the wave's lanes; -1 where it has no result of its own to
+// take part in: no tokens, fewer than are shared, or numbers above their bounds.
+__device__ __forceinline__ int shared_tokens(const SharedArgs &a, int seq, int len) {
+    const int lane = threadIdx.x & 63;
+    int shared = 0;
+    for (int g0 = 0; g0 < a.n_groups; g0 += 64) {
+        const int g = min(g0 + lane, a.n_groups - 1);
+        const int first = a.starts[g], end = a.starts[g + 1], n = a.shared[g];
+        const uint64_t mine = __ballot(first <= seq && seq < end);
+        if (mine != 0) {
+            shared = max(__builtin_amdgcn_readlane(n, __builtin_ctzll(mine)), 0);
+            break;
+        }
+    }
+    const bool fine = len > 0 && len <= a.max_len && shared <= a.max_shared && len >= shared && len - shared <= a.max_own;
+    return fine ? shared : -1;
+}
+
 // TILED: a page holds whole sub-tiles (page_size a multiple of 16) and scales
 // of neighbouring tokens lie side by side, so a sub-tile's page is looked up
 // once, in scalar registers.  Otherwise lane l finds the row (and reads the
 // scales) of the tile's token l % 32, and lanes take them from one another.
-template <int D, bool I8, bool TILED>
-__global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode_kernel(const AttnArgs a) {
+// With SharedArgs the tokens that a sequence has of its own, behind those that
+// its group shares, always to partial results.
+template <int D, bool I8, bool TILED, class ARGS = AttnArgs>
+__global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode_kernel(const ARGS a) {
+    constexpr bool SHARED = std::is_same_v<ARGS, SharedArgs>;
     constexpr int ES = I8 ? 1 : 2;         // bytes of a key or value element
     constexpr int STEPS = D / 32;          // products over the head dimension
     constexpr int DPL = D / 16;            // dims of a lane's V row piece = tiles of O^T
@@ -162,7 +185,8 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
     const int ht = b % a.head_tiles;
     b /= a.head_tiles;
     const int kvh = b % a.n_kv;
-    const int seq = b / a.n_kv;
+    int seq = b / a.n_kv;
+    if constexpr (SHARED) seq += a.seq0;
 
     const int head0 = kvh * a.group + ht * kAttnHeads;
     const int nh = min(kAttnHeads, a.group - ht * kAttnHeads);
@@ -173,7 +197,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
     const int len_in = *(cint_t *)(uintptr_t)(a.lens + seq);
     const int tbeg = chunk * a.chunk_tiles;
     int first_page[2] = {0, 0};
-    if (TILED && a.window == 0) {
+    if (TILED && !SHARED && a.window == 0) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int t = min(kAttnTile * (tbeg + wave) + 16 * u, a.max_len - 1);
@@ -198,8 +222,15 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
     asm volatile("" ::: "memory");  // (keeps the loads of q ahead of those of K and V, which it does not wait for)
 
     const bool too_long = len_in > a.max_len;
-    const AttnSpan sp = attn_span(len_in < 0 ? 0 : too_long ? 0 : len_in, a.window, a.sinks);
-    if (sp.tiles == 0) {
+    AttnSpan sp;
+    if constexpr (SHARED) {
+        const int shared = shared_tokens(a, seq, len_in);
+        if (shared < 0 || len_in <= shared) return;
+        sp = own_span(len_in, shared);
+    } else {
+        sp = attn_span(len_in < 0 ? 0 : too_long ? 0 : len_in, a.window, a.sinks);
+    }
+    if (!SHARED && sp.tiles == 0) {
         // no token to see: zeros (NaN where the length is past max_len)
         if (chunk == 0) {
             const float z = too_long ? __builtin_nanf("") : 0.0f;
@@ -470,7 +501,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
     int v = tbeg + wave;
     if (v < tend) {
         At at;
-        if (TILED && a.window == 0) {
+        if (TILED && !SHARED && a.window == 0) {
             const bool both = kAttnTile * v + 16 < sp.len;
 #pragma unroll
             for (int u = 0; u < (TILED ? 2 : 1); ++u) {
@@ -530,7 +561,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
             for (int e = 0; e < 4; ++e) acc[e] += f * x[e];
         }
         const int head = head0 + h;
-        if (sp.tiles <= a.chunk_tiles) {
+        if (!SHARED && sp.tiles <= a.chunk_tiles) {
             // the only chunk
             const int64_t at = seq * a.y_seq + head * a.y_head + d;
 #pragma unroll
@@ -540,7 +571,10 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
                 else static_cast<float *>(a.y)[at + e] = y;
             }
         } else {
-            float *part = a.part + ((int64_t)(seq * (int64_t)a.n_heads + head) * a.nchunks + chunk) * attn_part_floats(D);
+            int64_t slot;
+            if constexpr (SHARED) slot = (int64_t)(seq * (int64_t)a.n_heads + head) * a.slots + a.prefix_chunks + chunk;
+            else slot = (int64_t)(seq * (int64_t)a.n_heads + head) * a.nchunks + chunk;
+            float *part = a.part + slot * attn_part_floats(D);
             if (d == 0) {
                 part[0] = mm;
                 part[1] = ll;

@@ -1,0 +1,557 @@
+// attn_shared_impl.h - attention of one new token per sequence where groups of
+// sequences share their first tokens (gfx950): those are read once per group.
+//
+// Three launches.  The prefix kernel takes the shared tokens for all query
+// rows of a group (every sequence's heads that share a key-value head: a
+// matrix product instead of a product per row), the decode kernel takes each
+// sequence's own tokens, and both leave partial results (running maximum, sum
+// and output) that the join combines.
+//
+// Prefix kernel: a workgroup of four waves takes a tile of query rows over one
+// chunk of the shared tokens.  Keys and values go through LDS in tiles, keys
+// as they are and values transposed, so that both products read their operands
+// 16 bytes at a time, and v_mfma_f32_32x32x16 takes 32 rows per wave:
+//   S^T (tokens x rows) = K Q^T,  O^T (dims x rows) += V^T P^T.
+// Of a result tile lane (g = lane / 32, j = lane % 32) has row j and tokens
+// 8 (r / 4) + 4 g + r % 4; the second product's right operand wants eight tokens of
+// one g in a lane, and since their order is free as long as both operands have
+// the same, the values' tokens are stored in the order that the results have.
+// The next tile's rows are in registers while one is worked on.
+// 128 rows (every wave all tokens of a tile of 64) or, where a group has few,
+// 32 (every wave a quarter of the tokens of 128, joined in LDS at the end).
+//
+// Scores as in the decode kernel: exact keys, q in two fp16 parts.  The low
+// part is never 0 beside a high part that is not, so that a key which
+// overflowed to infinity keeps its sign.  Probabilities: with 8-bit values
+// all 24 bits in three bf16 parts; with fp16 values two fp16 parts of 2^15 p,
+// which holds p within 2^-21 of itself and 2^-39 of the row's largest (the exact form,
+// v_mfma_f32_16x16x4_f32, has an eighth of the rate, and this kernel is bound
+// by its products).
+#pragma once
+
+#include "attn_impl.h"
+
+namespace qk {
+
+typedef float f16_t __attribute__((ext_vector_type(16)));
+
+template <int D, int BN>
+struct PrefixLds {
+    static constexpr int kRow = 2 * D + 16;    // bytes of a key row (the 16 keep 16-byte reads of 16 rows off each other's banks)
+    static constexpr int kDim = 2 * BN + 16;   // bytes of a dimension's values
+    static constexpr int kValues = BN * kRow;
+    static constexpr int kPlaces = kValues + D * kDim;     // places of the next two tiles' rows
+    static constexpr int kScales = kPlaces + 2 * BN * 8;   // scales of the tile's keys, then values
+    static constexpr int kBytes = kScales + 2 * BN * 4;
+};
+
+// Sum and largest of the two lanes that share lane % 32.
+__device__ __forceinline__ float pair_max(float v) {
+    const u2_t r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+__device__ __forceinline__ float pair_sum(float v) {
+    const u2_t r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+
+template <int D, bool I8, bool WIDE>
+__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prefix_kernel(const SharedArgs a) {
+    constexpr int ROWS = prefix_rows(WIDE), BN = prefix_tokens(WIDE);
+    constexpr int WN = 128 / ROWS;             // waves that take different tokens of the same rows
+    constexpr int SUBS = BN / WN / 32;         // 32-token blocks of a wave
+    constexpr int ES = I8 ? 1 : 2;
+    constexpr int KS = D / 16, DB = D / 32;    // steps of the first product; blocks of output dims
+    constexpr int NQ = BN / 4;                 // quads of tokens
+    constexpr int UNITS = NQ * (D / 8);        // four tokens by eight dims each
+    constexpr int NU = (UNITS + 255) / 256;    // of a thread
+    using L = PrefixLds<D, BN>;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    int64_t *places = reinterpret_cast<int64_t *>(lds + L::kPlaces);
+    float *scales = reinterpret_cast<float *>(lds + L::kScales);
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 5, j = lane & 31;
+    const int wn = WIDE ? 0 : wave, row0 = WIDE ? 32 * wave : 0;
+
+    // The row tiles of one chunk and head are neighbours on one XCD, whose L2
+    // then has the chunk's rows for all of them but the first.
+    const int units = a.n_kv * a.prefix_chunks;
+    const int x = blockIdx.x & 7, y = blockIdx.x >> 3;
+    const int unit = y / a.row_tiles * 8 + x;
+    if (unit >= units) return;
+    const int kvh = unit % a.n_kv, chunk = unit / a.n_kv;
+    int tile = y % a.row_tiles + a.tile0;
+
+    // the group that the row tile is of
+    int first = 0, rows = 0, shared = 0;
+    {
+        bool is = false;
+        for (int g0 = 0; g0 < a.n_groups && !is; g0 += 64) {
+            const int gi = g0 + lane;
+            int at = 0, n = 0, sh = 0;
+            if (gi < a.n_groups) {
+                at = min(max(a.starts[gi], 0), a.n_seqs);
+                n = (min(max(a.starts[gi + 1], at), a.n_seqs) - at) * a.group;
+                sh = a.shared[gi];
+            }
+            const int tiles = (n + ROWS - 1) / ROWS;
+            int upto = tiles;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int u = __shfl_up(upto, d);
+                if (lane >= d) upto += u;
+            }
+            const uint64_t past = __ballot(upto > tile);
+            if (past != 0) {
+                const int src = __builtin_ctzll(past);
+                first = __builtin_amdgcn_readlane(at, src);
+                rows = __builtin_amdgcn_readlane(n, src);
+                shared = __builtin_amdgcn_readlane(sh, src);
+                tile -= __builtin_amdgcn_readlane(upto, src) - __builtin_amdgcn_readlane(tiles, src);
+                is = true;
+            } else {
+                tile -= __builtin_amdgcn_readlane(upto, 63);
+            }
+        }
+        // (a tile that is not there, and whatever groups out of order lead to)
+        if (!is || tile < 0 || (int64_t)tile * ROWS >= rows) return;
+    }
+    if (shared <= 0 || shared > a.max_shared) return;
+    const int64_t chunk_tokens = (int64_t)a.prefix_tiles * BN;
+    if (chunk * chunk_tokens >= shared) return;
+    const int t0 = (int)(chunk * chunk_tokens);
+    const int t1 = (int)min((int64_t)shared, t0 + chunk_tokens);
+    const int ntiles = (t1 - t0 + BN - 1) / BN;
+    const int wrow = tile * ROWS + row0;               // the wave's first row
+    const int left = rows - wrow;                      // of its 32
+    const int row = wrow + min(j, max(left, 1) - 1);   // lane's (one that is there)
+    const int member = row / a.group;
+    const int seq = first + min(member, rows / a.group - 1);
+    const int head = kvh * a.group + row - member * a.group;
+
+    // places of the rows of a tile's tokens, one thread each; past the end
+    // the last token's again
+    const int32_t *table = a.table + first * a.ld_table;
+    uint32_t bad = 0;
+    auto token_of = [&](int n) { return (int)min((int64_t)t0 + (int64_t)n * BN + tid, (int64_t)t1 - 1); };
+    auto page_of = [&](int t) { return (int)((uint64_t)(uint32_t)t * a.page_magic >> a.page_shift); };
+    float sc0[2] = {0.0f, 0.0f}, sc1[2] = {0.0f, 0.0f};   // scales of this tile's token and of the next one's
+    auto place = [&](int n, int id, float (&sc)[2]) __attribute__((always_inline)) {
+        const bool out = (unsigned)id >= (unsigned)a.n_pages;
+        bad |= out ? 1u : 0u;
+        const int t = token_of(n), page = out ? 0 : id;
+        const int slot = t - page_of(t) * a.page_size;
+        places[(n & 1) * BN + tid] = page * a.page_stride + kvh * a.head_stride + slot * a.slot_stride;
+        if constexpr (I8) {
+            const int64_t at = page * a.sc_page + kvh * a.sc_head + slot * a.sc_slot;
+            sc[0] = a.ks[at];
+            sc[1] = a.vs[at];
+        }
+    };
+
+    struct Quad { uint32_t k[4][2 * ES], v[4][2 * ES]; } reg[NU];
+    auto unit_at = [&](int u, int &quad, int &piece) {
+        quad = (u >> 2) % NQ;
+        piece = 4 * ((u >> 2) / NQ) + (u & 3);
+    };
+    auto load = [&](int n) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+            const int u = tid + 256 * i;
+            if (UNITS % 256 != 0 && u >= UNITS) continue;
+            int quad, piece;
+            unit_at(u, quad, piece);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int64_t at = places[(n & 1) * BN + 4 * quad + e] + 8 * ES * piece;
+                __builtin_memcpy(reg[i].k[e], a.k + at, 8 * ES);
+                __builtin_memcpy(reg[i].v[e], a.v + at, 8 * ES);
+            }
+        }
+    };
+    auto store = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+            const int u = tid + 256 * i;
+            if (UNITS % 256 != 0 && u >= UNITS) continue;
+            int quad, piece;
+            unit_at(u, quad, piece);
+            const int pos = 16 * (quad >> 2) + 8 * (quad & 1) + 2 * (quad & 2);  // of the quad's tokens in the results' order
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                h8_t kk;
+                if constexpr (I8) kk = codes8_f16(reg[i].k[e][0], reg[i].k[e][1]);
+                else __builtin_memcpy(&kk, reg[i].k[e], 16);
+                *reinterpret_cast<h8_t *>(lds + (4 * quad + e) * L::kRow + 16 * piece) = kk;
+            }
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+                u2_t w;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if constexpr (I8) {
+                        const float e0 = (float)(int8_t)(reg[i].v[2 * h][d / 4] >> (8 * (d % 4)));
+                        const float e1 = (float)(int8_t)(reg[i].v[2 * h + 1][d / 4] >> (8 * (d % 4)));
+                        w[h] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, e1), __builtin_bit_cast(uint32_t, e0), 0x07060302u);
+                    } else {
+                        w[h] = __builtin_amdgcn_perm(reg[i].v[2 * h + 1][d / 2], reg[i].v[2 * h][d / 2],
+                                                     d % 2 ? 0x07060302u : 0x05040100u);
+                    }
+                }
+                *reinterpret_cast<u2_t *>(lds + L::kValues + (8 * piece + d) * L::kDim + 2 * pos) = w;
+            }
+        }
+    };
+
+    int id = 0;
+    if (tid < BN) {
+        const int p0 = table[page_of(token_of(0))], p1 = table[page_of(token_of(1))];
+        id = table[page_of(token_of(2))];
+        place(0, p0, sc0);
+        place(1, p1, sc1);
+    }
+    __syncthreads();
+    load(0);
+
+    // q in two parts
+    h8_t qh[KS], ql[KS];
+    int qexp;
+    {
+        float qv[KS][8];
+        const float *q = a.q + seq * a.q_seq + head * a.q_head + 8 * g;
+        float top = 0.0f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) __builtin_memcpy(qv[s], q + 16 * s, 32);
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                qv[s][i] *= a.qscale;
+                top = fmaxf(top, fabsf(qv[s][i]));
+            }
+        top = pair_max(top);
+        int ex = 14;
+        if (top > 0.0f && top <= 3.402823466e38f) (void)frexpf(top, &ex);
+        qexp = ex - 14;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) qv[s][i] = ldexpf(qv[s][i], -qexp);
+            split8(qv[s], qh[s], ql[s]);
+            if constexpr (!I8) {
+                // (2^-14 for a low part of 0: 2^-27 of the row's largest)
+                u4_t h = __builtin_bit_cast(u4_t, qh[s]), l = __builtin_bit_cast(u4_t, ql[s]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if ((l[i] & 0x7FFFu) == 0 && (h[i] & 0x7FFFu) != 0) l[i] |= 0x0400u | (h[i] & 0x8000u);
+                    if ((l[i] & 0x7FFF0000u) == 0 && (h[i] & 0x7FFF0000u) != 0) l[i] |= 0x04000000u | (h[i] & 0x80000000u);
+                }
+                ql[s] = __builtin_bit_cast(h8_t, l);
+            }
+        }
+        if constexpr (I8) qexp += 9;  // codes are held times 2^-9
+    }
+
+    constexpr float LIFT = I8 ? 0.0f : 15.0f;   // probabilities are held times 2^LIFT
+    f16_t o[DB];
+#pragma unroll
+    for (int c = 0; c < DB; ++c)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[c][r] = 0.0f;
+    float m = kAttnLow, l = 0.0f;               // m: the running maximum less LIFT
+
+    for (int n = 0; n < ntiles; ++n) {
+        __syncthreads();   // (the last tile and its places are read)
+        store();
+        if (tid < BN) {
+            if constexpr (I8) {
+                scales[tid] = sc0[0];
+                scales[BN + tid] = sc0[1];
+                sc0[0] = sc1[0];
+                sc0[1] = sc1[1];
+            }
+            place(n + 2, id, sc1);
+        }
+        __syncthreads();
+        if (tid < BN) id = table[page_of(token_of(n + 3))];
+        if (n + 1 < ntiles) load(n + 1);
+        if (left <= 0) continue;
+#pragma unroll
+        for (int sub = 0; sub < SUBS; ++sub) {
+            const int b0 = (SUBS * wn + sub) * 32;   // the block's first token in the tile
+            const int here = t1 - t0 - n * BN - b0;  // tokens from there on
+            if (here <= 0) continue;
+            f16_t c;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) c[r] = 0.0f;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const h8_t kk = *reinterpret_cast<const h8_t *>(lds + (b0 + j) * L::kRow + 32 * s + 16 * g);
+                c = __builtin_amdgcn_mfma_f32_32x32x16_f16(kk, qh[s], c, 0, 0, 0);
+                c = __builtin_amdgcn_mfma_f32_32x32x16_f16(kk, ql[s], c, 0, 0, 0);
+            }
+            float p[16];
+            float top = kAttnLow;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                p[r] = ldexpf(c[r], qexp);
+                if constexpr (I8) p[r] *= scales[b0 + 8 * (r >> 2) + 4 * g + (r & 3)];
+            }
+            if (here < 32) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (8 * (r >> 2) + 4 * g + (r & 3) >= here) p[r] = kAttnLow;
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, p[r]);
+            top = pair_max(top) - LIFT;
+            if (__any(top > m)) {
+                const float mn = fmaxf(m, top);
+                const float f = __builtin_amdgcn_exp2f(m - mn);
+                l *= f;
+                m = mn;
+#pragma unroll
+                for (int c2 = 0; c2 < DB; ++c2)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) o[c2][r] *= f;
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                p[r] = __builtin_amdgcn_exp2f(p[r] - m);
+                if (here < 32 && 8 * (r >> 2) + 4 * g + (r & 3) >= here) p[r] = 0.0f;
+                l += p[r];
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                float ps[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ps[i] = p[8 * s + i];
+                const uint8_t *at = lds + L::kValues + j * L::kDim + 2 * (b0 + 16 * s + 8 * g);
+                if constexpr (I8) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        ps[i] *= scales[BN + b0 + 16 * s + 8 * (i >> 2) + 4 * g + (i & 3)];
+                        // (the scale of a token past the end is the last one's: 0 where that is not finite)
+                        if (here < 32 && 16 * s + 8 * (i >> 2) + 4 * g + (i & 3) >= here) ps[i] = 0.0f;
+                    }
+                    b8_t part[3];
+                    split8_bf16(ps, part);
+#pragma unroll
+                    for (int c2 = 0; c2 < DB; ++c2) {
+                        const b8_t vv = *reinterpret_cast<const b8_t *>(at + 32 * c2 * L::kDim);
+#pragma unroll
+                        for (int e = 0; e < 3; ++e) o[c2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vv, part[e], o[c2], 0, 0, 0);
+                    }
+                } else {
+                    h8_t hi, lo;
+                    split8(ps, hi, lo);
+#pragma unroll
+                    for (int c2 = 0; c2 < DB; ++c2) {
+                        const h8_t vv = *reinterpret_cast<const h8_t *>(at + 32 * c2 * L::kDim);
+                        o[c2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv, hi, o[c2], 0, 0, 0);
+                        o[c2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv, lo, o[c2], 0, 0, 0);
+                    }
+                }
+            }
+        }
+    }
+    l = pair_sum(l);
+    if (__syncthreads_or(bad)) l = __builtin_nanf("");
+
+    if constexpr (!WIDE) {
+        // the waves' results, the first one's registers taking them all
+        float *other = reinterpret_cast<float *>(lds);
+        constexpr int PER = (16 * DB + 2) * 64;
+        if (wave > 0) {
+            float *mine = other + (wave - 1) * PER;
+#pragma unroll
+            for (int c = 0; c < DB; ++c)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) mine[(16 * c + r) * 64 + lane] = o[c][r];
+            mine[16 * DB * 64 + lane] = m;
+            mine[(16 * DB + 1) * 64 + lane] = l;
+        }
+        __syncthreads();
+        if (wave > 0) return;
+        float ms[WN], mm = m;
+#pragma unroll
+        for (int w = 1; w < WN; ++w) {
+            ms[w] = other[(w - 1) * PER + 16 * DB * 64 + lane];
+            mm = fmaxf(mm, ms[w]);
+        }
+        const float f0 = __builtin_amdgcn_exp2f(m - mm);
+        l *= f0;
+#pragma unroll
+        for (int c = 0; c < DB; ++c)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[c][r] *= f0;
+#pragma unroll
+        for (int w = 1; w < WN; ++w) {
+            const float f = __builtin_amdgcn_exp2f(ms[w] - mm);
+            const float *from = other + (w - 1) * PER + lane;
+            l += f * from[(16 * DB + 1) * 64];
+#pragma unroll
+            for (int c = 0; c < DB; ++c)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[c][r] += f * from[(16 * c + r) * 64];
+        }
+        m = mm;
+    }
+    if (j >= left) return;
+    float *part = a.part + ((int64_t)(seq * (int64_t)a.n_heads + head) * a.slots + chunk) * attn_part_floats(D);
+    if (g == 0) {
+        part[0] = m;
+        part[1] = l;
+    }
+#pragma unroll
+    for (int c = 0; c < DB; ++c)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            *reinterpret_cast<f4_t *>(part + 4 + 32 * c + 8 * r + 4 * g) =
+                f4_t{o[c][4 * r], o[c][4 * r + 1], o[c][4 * r + 2], o[c][4 * r + 3]};
+}
+
+// Joins the partial results of one (sequence, head): those of the shared
+// tokens' chunks, then those of its own.
+template <int D>
+__global__ __launch_bounds__(256) void attn_shared_join_kernel(const SharedArgs a) {
+    constexpr int COLS = D / 4;
+    constexpr int ROWS = 256 / COLS;   // chunks at a time
+    constexpr int U = kAttnJoinUnroll;
+    __shared__ __attribute__((aligned(16))) float so[ROWS][D];
+    __shared__ float sl[ROWS], sm[ROWS];
+    const int head = blockIdx.x % a.n_heads;
+    const int seq = blockIdx.x / a.n_heads + a.seq0;
+    const int len = a.lens[seq];
+    const int shared = shared_tokens(a, seq, len);
+    // groups out of order have no result
+    bool order = true;
+    for (int g = threadIdx.x & 63; g < a.n_groups; g += 64) {
+        const int first = a.starts[g], end = a.starts[g + 1];
+        order = order && first >= 0 && first <= end && end <= a.n_seqs;
+    }
+    const bool in_order = __all(order);
+    const bool fine = in_order && shared >= 0;
+    const int row = threadIdx.x / COLS, col = threadIdx.x % COLS;
+    int n1 = 0, n = 0;
+    if (fine) {
+        const int64_t chunk = (int64_t)a.prefix_tiles * prefix_tokens(a.wide);
+        n1 = shared > 0 ? (int)((shared + chunk - 1) / chunk) : 0;
+        n = n1 + (len > shared ? (own_span(len, shared).tiles + a.chunk_tiles - 1) / a.chunk_tiles : 0);
+    }
+    const float *part = a.part + (int64_t)(seq * (int64_t)a.n_heads + head) * a.slots * attn_part_floats(D);
+    if (row < ROWS && n > 0) {
+        f4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        float l = 0.0f, m = kAttnLow;
+        for (int c0 = row; c0 < n; c0 += U * ROWS) {
+            float pm[U], pl[U];
+            f4_t x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                // (past the last chunk: the last one again, with weight 0)
+                const int c = min(c0 + u * ROWS, n - 1);
+                const float *p = part + (c < n1 ? c : a.prefix_chunks + c - n1) * attn_part_floats(D);
+                __builtin_memcpy(&x[u], p + 4 + 4 * col, 16);
+                pm[u] = p[0];
+                pl[u] = p[1];
+            }
+            float top = m;
+#pragma unroll
+            for (int u = 0; u < U; ++u) top = fmaxf(top, pm[u]);
+            const float f0 = __builtin_amdgcn_exp2f(m - top);
+            l *= f0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] *= f0;
+            m = top;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (c0 + u * ROWS >= n) continue;
+                const float f = __builtin_amdgcn_exp2f(pm[u] - top);
+                l += f * pl[u];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[e] += f * x[u][e];
+            }
+        }
+        *reinterpret_cast<f4_t *>(&so[row][4 * col]) = acc;
+        if (col == 0) {
+            sl[row] = l;
+            sm[row] = m;
+        }
+    }
+    __syncthreads();
+    for (int d = threadIdx.x; d < D; d += 256) {
+        float y = __builtin_nanf("");
+        if (n > 0) {
+            float m = sm[0];
+            for (int r = 1; r < ROWS; ++r) m = fmaxf(m, sm[r]);
+            float acc = 0.0f, l = 0.0f;
+            for (int r = 0; r < ROWS; ++r) {
+                const float f = __builtin_amdgcn_exp2f(sm[r] - m);
+                acc += f * so[r][d];
+                l += f * sl[r];
+            }
+            y = acc / l;
+        } else if (len <= 0 && in_order) {
+            y = 0.0f;
+        }
+        const int64_t at = seq * a.y_seq + head * a.y_head + d;
+        if (a.out_f16) static_cast<uint16_t *>(a.y)[at] = f2h(y);
+        else static_cast<float *>(a.y)[at] = y;
+    }
+}
+
+template <int D, bool I8, bool WIDE>
+int attn_prefix_launch(const SharedArgs &a, hipStream_t stream) {
+    constexpr size_t bytes = PrefixLds<D, prefix_tokens(WIDE)>::kBytes;
+    const auto kern = attn_prefix_kernel<D, I8, WIDE>;
+    if (bytes > 65536 && hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)bytes) != hipSuccess)
+        return QK_ERR_LAUNCH;
+    const int64_t units = ((int64_t)a.n_kv * a.prefix_chunks + 7) / 8 * 8;
+    const int64_t most = max_groups(256) / units;  // row tiles of one launch
+    for (int64_t tile = 0; tile < a.row_tiles; tile += most) {
+        SharedArgs p = a;
+        p.tile0 = (int)tile;
+        p.row_tiles = (int)std::min<int64_t>(a.row_tiles - tile, most);
+        const int st = launch_lds(kern, dim3((unsigned)(units * p.row_tiles)), dim3(256), bytes, stream, p);
+        if (st != QK_OK) return st;
+    }
+    return QK_OK;
+}
+
+template <int D, bool I8>
+int attn_shared_dim(const SharedArgs &a, bool tiled, hipStream_t stream) {
+    int st = QK_OK;
+    if (a.prefix_chunks > 0) st = a.wide ? attn_prefix_launch<D, I8, true>(a, stream) : attn_prefix_launch<D, I8, false>(a, stream);
+    const int64_t rows = (int64_t)a.n_kv * a.head_tiles * a.nchunks;
+    const int64_t most = std::max<int64_t>(1, max_groups(256) / std::max<int64_t>(rows, a.n_heads));  // sequences of one launch
+    for (int64_t seq = 0; seq < a.n_seqs && st == QK_OK; seq += most) {
+        SharedArgs p = a;
+        p.seq0 = (int)seq;
+        const int64_t n = std::min<int64_t>(a.n_seqs - seq, most);
+        const dim3 grid((unsigned)(n * rows)), block(64 * kAttnWaves);
+        st = tiled ? launch(attn_decode_kernel<D, I8, true, SharedArgs>, grid, block, stream, p)
+                   : launch(attn_decode_kernel<D, I8, false, SharedArgs>, grid, block, stream, p);
+        if (st == QK_OK) st = launch(attn_shared_join_kernel<D>, dim3((unsigned)(n * a.n_heads)), dim3(256), stream, p);
+    }
+    return st;
+}
+
+template <bool I8>
+int attn_shared_run(const SharedArgs &a, int head_dim, bool tiled, hipStream_t stream) {
+    switch (head_dim) {
+    case 32: return attn_shared_dim<32, I8>(a, tiled, stream);
+    case 64: return attn_shared_dim<64, I8>(a, tiled, stream);
+    case 96: return attn_shared_dim<96, I8>(a, tiled, stream);
+    case 128: return attn_shared_dim<128, I8>(a, tiled, stream);
+    case 160: return attn_shared_dim<160, I8>(a, tiled, stream);
+    case 192: return attn_shared_dim<192, I8>(a, tiled, stream);
+    case 224: return attn_shared_dim<224, I8>(a, tiled, stream);
+    case 256: return attn_shared_dim<256, I8>(a, tiled, stream);
+    default: return QK_ERR_INVALID_ARG;
+    }
+}
+
+}  // namespace qk

@@ -24,7 +24,7 @@ SYMBOLS = ("qk_block_bytes", "qk_row_bytes", "qk_status_string", "qk_version",
            "qk_dequantize", "qk_mul_mat_vec", "qk_mul_mat_vec_x8", "qk_mul_mat_vec_batched",
            "qk_mul_mat_vec_id", "qk_mul_mat", "qk_mul_mat_vec_x8q", "qk_rms_norm", "qk_kv_store",
            "qk_attn_decode", "qk_attn_decode_workspace", "qk_moe_route", "qk_kv_copy", "qk_kv_fork", "qk_kv_compact",
-           "qk_kv_pages_workspace", "qk_token_logprobs", "qk_token_logprobs_workspace")
+           "qk_kv_pages_workspace", "qk_attn_decode_shared", "qk_attn_decode_shared_workspace", "qk_token_logprobs", "qk_token_logprobs_workspace")
 QK_MAX_BATCH = 16
 X8_BLOCK_BYTES = 36  # an 8-bit activation block: fp32 scale, 32 int8 codes
 
@@ -111,6 +111,11 @@ def load():
     lib.qk_kv_compact.restype = ci
     lib.qk_kv_pages_workspace.argtypes = [i64, i64]
     lib.qk_kv_pages_workspace.restype = ctypes.c_size_t
+    lib.qk_attn_decode_shared.argtypes = [cache, vp, i64, i64, i64, i64, vp, i64, vp, i64, vp, vp, i64, i64, i64,
+                                          ctypes.c_float, ci, vp, i64, i64, vp, ctypes.c_size_t, vp]
+    lib.qk_attn_decode_shared.restype = ci
+    lib.qk_attn_decode_shared_workspace.argtypes = [cache, i64, i64, i64, i64, i64]
+    lib.qk_attn_decode_shared_workspace.restype = ctypes.c_size_t
     lib.qk_token_logprobs.argtypes = [ci, vp, i64, i64, i64, ctypes.c_float, vp, i64, i64, vp, i64, vp, i64, vp, i64,
                                       vp, i64, vp, ctypes.c_size_t, vp]
     lib.qk_token_logprobs.restype = ci
@@ -247,6 +252,19 @@ def qk_kv_compact(table_ptr, ld_table, lens_ptr, n_rows, max_pages, page_size, n
 
 def qk_kv_pages_workspace(n_rows, n_pages):
     return load().qk_kv_pages_workspace(n_rows, n_pages)
+
+
+def qk_attn_decode_shared(cache, q_ptr, q_seq, q_head, n_seqs, n_q_heads, table_ptr, ld_table, lens_ptr, max_len,
+                          starts_ptr, shared_ptr, n_groups, max_shared, max_own, scale, y_dtype, y_ptr, y_seq, y_head,
+                          workspace_ptr, workspace_bytes, stream=0):
+    """cache: a KVCacheDesc or None."""
+    return load().qk_attn_decode_shared(cache, q_ptr, q_seq, q_head, n_seqs, n_q_heads, table_ptr, ld_table, lens_ptr,
+                                        max_len, starts_ptr, shared_ptr, n_groups, max_shared, max_own, scale, y_dtype,
+                                        y_ptr, y_seq, y_head, workspace_ptr, workspace_bytes, stream)
+
+
+def qk_attn_decode_shared_workspace(cache, n_seqs, n_q_heads, max_len, max_shared, max_own):
+    return load().qk_attn_decode_shared_workspace(cache, n_seqs, n_q_heads, max_len, max_shared, max_own)
 
 
 def qk_token_logprobs(x_dtype, logits_ptr, ldx, n, vocab, scale, ids_ptr, ld_ids, n_ids, logprobs_ptr, ld_logprobs,
@@ -935,6 +953,68 @@ def kv_compact(table, lens, page_size, n_pages, out=None, workspace=None, stream
                               live.data_ptr(), work, size, _stream_of(table))
     _check(st, "qk_kv_compact")
     return out, src, dst, live
+
+
+def attn_decode_shared_workspace(cache, n_seqs, n_q_heads, max_len, max_shared=None, max_own=None):
+    """Scratch for attn_decode_shared calls of up to these sizes in any groups:
+    a uint8 tensor.  One tensor serves one stream at a time."""
+    import torch
+    max_shared = max_len if max_shared is None else max_shared
+    need = qk_attn_decode_shared_workspace(cache.desc, n_seqs, n_q_heads, max_len, max_shared,
+                                           max_len if max_own is None else max_own)
+    return torch.empty(need, dtype=torch.uint8, device=cache.device) if need else None
+
+
+def attn_decode_shared(cache, q, table, lens, starts, shared, scale=None, max_len=None, max_shared=None, max_own=None,
+                       out_dtype="f32", y=None, workspace=None, stream=None):
+    """attn_decode for a batch in which groups of sequences share their first
+    tokens, which are read once per group: group g is sequences starts[g] ..
+    starts[g + 1] - 1, and each begins with the shared[g] tokens in the pages of
+    the first of them.  starts int32 (n_groups + 1,), ascending; shared int32
+    (n_groups,).  max_shared and max_own bound shared and lens - shared (default:
+    max_len) and size the split.  Other arguments and y as attn_decode."""
+    import torch
+    if stream is not None:
+        return _on_stream(stream, q, attn_decode_shared, cache, q, table, lens, starts, shared, scale, max_len, max_shared,
+                          max_own, out_dtype, y, workspace)
+    if out_dtype not in ("f32", "f16"):
+        raise ValueError(f"out_dtype must be 'f32' or 'f16', got {out_dtype!r}")
+    code, dt = (QK_F32, torch.float32) if out_dtype == "f32" else (QK_F16, torch.float16)
+    _table_check(table, lens)
+    _int32_check(starts, "starts", 1)
+    _int32_check(shared, "shared", 1)
+    if starts.shape[0] != shared.shape[0] + 1:
+        raise ValueError(f"starts has {starts.shape[0]} entries for {shared.shape[0]} groups (one more than groups)")
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise TypeError("q must be a float32 tensor (n_seqs, n_q_heads, head_dim)")
+    n, heads, dim = q.shape[0], q.shape[1], cache.head_dim
+    _heads_check(q, "q", torch.float32, n, heads, dim)
+    if heads < 1 or heads % cache.n_heads != 0:
+        raise ValueError(f"{heads} query heads over {cache.n_heads} key-value heads")
+    if table.shape[0] != n:
+        raise ValueError(f"q has {n} sequences, table {table.shape[0]}")
+    room = table.shape[1] * cache.page_size
+    max_len = room if max_len is None else int(max_len)
+    if not 1 <= max_len <= room:
+        raise ValueError(f"max_len {max_len}: the table has room for {room} tokens")
+    max_shared = max_len if max_shared is None else int(max_shared)
+    max_own = max_len if max_own is None else int(max_own)
+    if not 0 <= max_shared <= max_len or not 1 <= max_own <= max_len:
+        raise ValueError(f"max_shared {max_shared} and max_own {max_own} must be 0..{max_len} and 1..{max_len}")
+    if y is None:
+        y = q.new_empty((n, heads, dim), dtype=dt)
+    else:
+        _heads_check(y, "y", dt, n, heads, dim)
+    _on_device(cache.k, q, table, lens, starts, shared, y, workspace)
+    need = 0 if workspace is not None else qk_attn_decode_shared_workspace(cache.desc, n, heads, max_len, max_shared, max_own)
+    work, size = _ptr_bytes(_scratch(workspace, need, q.device))
+    q_head, y_head = (q.stride(1), y.stride(1)) if heads > 1 else (0, 0)
+    st = load().qk_attn_decode_shared(cache.desc, q.data_ptr(), _row_stride(q), q_head, n, heads, table.data_ptr(),
+                                      table.stride(0), lens.data_ptr(), max_len, starts.data_ptr(), shared.data_ptr(),
+                                      shared.shape[0], max_shared, max_own, dim ** -0.5 if scale is None else scale, code,
+                                      y.data_ptr(), _row_stride(y), y_head, work, size, _stream_of(q))
+    _check(st, "qk_attn_decode_shared")
+    return y
 
 
 def token_logprobs_workspace(n, vocab, top=0, device="cuda"):

@@ -532,6 +532,53 @@ size_t qk_attn_decode_workspace(const qk_kv_cache *cache, int64_t n_seqs, int64_
                                 int64_t max_len, int64_t window, int64_t sinks);
 
 /*
+ * qk_attn_decode_shared - qk_attn_decode for a batch in which groups of
+ * sequences share their first tokens (answers to one prompt, conversations
+ * behind one system prompt): the shared tokens are read once for a group
+ * instead of once for each of its sequences.
+ *
+ *   group g: sequences starts[g] .. starts[g + 1] - 1, of which each begins with
+ *   the shared[g] tokens that lie in the pages of the first of them
+ *
+ * The result is that of qk_attn_decode without a window, but for rounding:
+ * of another sequence's table only entries of pages with tokens of its own, at or
+ * behind shared[g], are followed.  Sequences of no group share nothing.
+ * lens[s] <= 0: zeros.  NaN: lens[s] above max_len or below shared[g], more
+ * shared tokens than max_shared, more of its own than max_own, or a page id
+ * outside the pool; and the whole batch where starts does not ascend within
+ * 0..n_seqs.  A negative shared[g] is 0, and a group may be empty.  The result
+ * does not depend on what sequences of other groups hold or on the order in
+ * which anything arrives; n_seqs, n_groups, max_shared and max_own decide the
+ * order of its sums.
+ * Scores as in qk_attn_decode.  Probabilities meet fp16 values in two fp16
+ * parts: within 2^-21 of themselves and 2^-39 of the row's largest; 8-bit
+ * values with all their 24 bits.  An fp16 value that overflowed to infinity may
+ * give NaN.
+ *
+ *   starts, shared   device int32[n_groups + 1] and int32[n_groups]; n_groups
+ *              >= 0 (NULL with 0)
+ *   max_len    1..2^30, no length is above it
+ *   max_shared, max_own   0..max_len and 1..max_len: bounds of shared[g] and of
+ *              lens[s] - shared[g]; the parts are sized for them
+ *   workspace  16-byte aligned device memory of the bytes that
+ *              qk_attn_decode_shared_workspace gives for these sizes or larger
+ *              ones; it need not be cleared
+ * Other arguments and errors as qk_attn_decode.
+ */
+int qk_attn_decode_shared(const qk_kv_cache *cache, const float *q, int64_t q_seq, int64_t q_head,
+                          int64_t n_seqs, int64_t n_q_heads, const int32_t *table, int64_t ld_table,
+                          const int32_t *lens, int64_t max_len, const int32_t *starts, const int32_t *shared,
+                          int64_t n_groups, int64_t max_shared, int64_t max_own, float scale,
+                          int y_dtype, void *y, int64_t y_seq, int64_t y_head,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that serve qk_attn_decode_shared with up to n_seqs
+ * sequences in any groups, and up to max_len, max_shared and max_own tokens,
+ * over this cache and with n_q_heads; 0 on a bad argument. */
+size_t qk_attn_decode_shared_workspace(const qk_kv_cache *cache, int64_t n_seqs, int64_t n_q_heads, int64_t max_len,
+                                       int64_t max_shared, int64_t max_own);
+
+/*
  * qk_moe_route - choose experts for tokens: the ids that qk_mul_mat_vec_id
  * takes, and their weights.
  *
