@@ -839,8 +839,8 @@ int qk_kv_compact(const int32_t *table, int64_t ld_table, const int32_t *lens, i
 static size_t logp_part_bytes(int64_t top) { return 16 + 8 * (size_t)top; }
 
 size_t qk_token_logprobs_workspace(int64_t n, int64_t vocab, int64_t top) {
-    if (n < 0 || n > kMaxDim || vocab < 1 || vocab > (1 << 30) || top < 0 || top > qk::kLogpMost) return 0;
-    return (size_t)qk::logp_parts_bound(n, vocab, qk::device_cus()) * logp_part_bytes(top);
+    if (n < 0 || n > kMaxDim || vocab < 1 || vocab > (1 << 30) || top < 0 || top > qk::kLogpTop) return 0;
+    return (size_t)qk::logp_parts(n, vocab) * logp_part_bytes(top);
 }
 
 int qk_token_logprobs(int x_dtype, const void *logits, int64_t ldx, int64_t n, int64_t vocab, float scale,
@@ -848,7 +848,7 @@ int qk_token_logprobs(int x_dtype, const void *logits, int64_t ldx, int64_t n, i
                       float *entropy, int64_t top, int32_t *best_ids, int64_t ld_best_ids, float *best, int64_t ld_best,
                       void *workspace, size_t workspace_bytes, void *stream) {
     if (x_dtype != QK_F32 && x_dtype != QK_F16) return QK_ERR_UNSUPPORTED;
-    if (n < 0 || vocab < 1 || vocab > (1 << 30) || n_ids < 0 || n_ids > (1 << 20) || top < 0 || top > qk::kLogpMost ||
+    if (n < 0 || vocab < 1 || vocab > (1 << 30) || n_ids < 0 || n_ids > (1 << 20) || top < 0 || top > qk::kLogpTop ||
         top > vocab || !(scale > 0.0f) || scale > 3.402823466e38f)
         return QK_ERR_INVALID_ARG;
     if (n == 0) return QK_OK;
@@ -867,9 +867,9 @@ int qk_token_logprobs(int x_dtype, const void *logits, int64_t ldx, int64_t n, i
     if ((uintptr_t)logits % es != 0 || ((uintptr_t)ids | (uintptr_t)logprobs | (uintptr_t)entropy | (uintptr_t)best_ids |
                                         (uintptr_t)best) % 4 != 0 || (uintptr_t)workspace % 16 != 0)
         return QK_ERR_ALIGNMENT;
-    const int each = qk::logp_each(n, vocab, qk::device_cus());
-    const int64_t parts = qk::logp_parts(vocab, each);
-    const size_t need = parts > 1 ? (size_t)n * parts * logp_part_bytes(top) : 0;
+    const qk::LogpSplit split = qk::logp_split(n, vocab, qk::device_cus());
+    const int64_t parts = split.parts(vocab);
+    const size_t need = (size_t)qk::logp_parts(n, vocab) * logp_part_bytes(top);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return QK_ERR_INVALID_ARG;
     const Range in[] = {{logits, span_bytes(n, ldx, vocab, es)}, {ids, span_bytes(n, ld_ids, n_ids, 4)}};
     const Range outs[] = {{logprobs, span_bytes(n, ld_logprobs, n_ids, 4)}, {entropy, entropy ? 4 * (size_t)n : 0},
@@ -898,11 +898,12 @@ int qk_token_logprobs(int x_dtype, const void *logits, int64_t ldx, int64_t n, i
     a.top = (int)top;
     a.parts = (int)parts;
     a.scale = scale;
+    a.scale2 = (float)std::min((double)scale * 1.4426950408889634, 3.402823466e38);
     if (need > 0) {
         a.stat = static_cast<float *>(workspace);
         a.list = reinterpret_cast<uint64_t *>(a.stat + 4 * n * parts);
     }
-    return qk::launch_token_logprobs(a, x_dtype == QK_F16, each, static_cast<hipStream_t>(stream));
+    return qk::launch_token_logprobs(a, x_dtype == QK_F16, split, static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

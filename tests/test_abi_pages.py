@@ -99,35 +99,23 @@ LOGP = dict(xt=E.QK_F32, x=A, ldx=100, n=4, vocab=100, scale=1.0, ids=B, ld_ids=
     (dict(ldx=99), BAD), (dict(ld_ids=1), BAD), (dict(ld_lp=1), BAD), (dict(ld_bi=4), BAD), (dict(ld_b=4), BAD),
     (dict(x=A + 2), ALIGN), (dict(xt=E.QK_F16, x=A + 1), ALIGN), (dict(ids=B + 2), ALIGN), (dict(lp=C + 1), ALIGN), (dict(entropy=D + 2), ALIGN),
     (dict(bi=F + 2), ALIGN), (dict(b=G + 2), ALIGN), (dict(lp=A), BAD), (dict(entropy=A + 1596), BAD), (dict(bi=B), BAD), (dict(b=F), BAD),
-    (dict(entropy=C), BAD), (dict(vocab=5000, ldx=5000), BAD), (dict(vocab=5000, ldx=5000, ws=WS, ws_bytes=8), BAD),
-    (dict(vocab=5000, ldx=5000, ws=WS + 8, ws_bytes=10000), ALIGN), (dict(vocab=5000, ldx=5000, ws=A, ws_bytes=10000), BAD),
-    (dict(vocab=5000, ldx=5000, ws=C, ws_bytes=10000), BAD), (dict(n=0), OK), (dict(n=0, x=None, ids=None), OK),
+    (dict(entropy=C), BAD), (dict(vocab=40000, ldx=40000), BAD), (dict(vocab=40000, ldx=40000, ws=WS, ws_bytes=8), BAD),
+    (dict(vocab=40000, ldx=40000, ws=WS + 8, ws_bytes=10000), ALIGN), (dict(vocab=40000, ldx=40000, ws=A, ws_bytes=10000), BAD),
+    (dict(vocab=40000, ldx=40000, ws=C, ws_bytes=10000), BAD), (dict(n=0), OK), (dict(n=0, x=None, ids=None), OK),
 ])
 def test_logprobs_refusals(kw, want):
     assert _call(qk.qk_token_logprobs, LOGP, kw) == want
 
 
-def _parts(n, vocab):
-    """Parts of all rows as the split is defined: 512 times 64 logits, halved
-    while a half holds a row or there are not two parts for each of 256 CUs."""
-    each = 64
-    while each > 8 and (512 * each // 2 >= vocab or n * -(-vocab // (512 * each)) < 512):
-        each //= 2
-    parts = -(-vocab // (512 * each))
-    return n * parts if parts > 1 else 0
-
-
-def test_logprobs_workspace_serves_smaller_calls():
+def test_logprobs_workspace():
+    """One entry for each 32768 logits of a row that has more; enough for any
+    smaller call."""
     assert qk.qk_token_logprobs_workspace(-1, 100, 1) == 0 and qk.qk_token_logprobs_workspace(1, 0, 1) == 0
-    assert qk.qk_token_logprobs_workspace(1, 100, 65) == 0 and qk.qk_token_logprobs_workspace(1, 4096, 20) == 0
-    rows = (1, 2, 15, 16, 31, 33, 64, 100, 130, 255, 256, 511, 512, 513, 1000, 5000)
-    vocabs = (1, 4096, 4097, 8192, 8193, 16384, 16385, 32000, 32768, 32769, 65537, 131072, 262144, 2 ** 21)
-    need = {(n, v): _parts(n, v) * (16 + 8 * 20) for n in rows for v in vocabs}
-    for n in rows:
-        for v in vocabs:
-            asked = qk.qk_token_logprobs_workspace(n, v, 20)
-            assert asked >= max(x for (m, u), x in need.items() if m <= n and u <= v), (n, v)
-            assert asked <= (16 + 8 * 20) * max(1024, n * -(-v // 32768)), (n, v)
+    assert qk.qk_token_logprobs_workspace(1, 100, 65) == 0 and qk.qk_token_logprobs_workspace(1, 32768, 20) == 0
+    for n in (1, 2, 512, 5000):
+        for v, parts in ((32769, 2), (65536, 2), (65537, 3), (2 ** 21, 64)):
+            for top in (0, 1, 64):
+                assert qk.qk_token_logprobs_workspace(n, v, top) == n * parts * (16 + 8 * top)
 
 
 def _cpu(*shape, dtype=torch.int32):
