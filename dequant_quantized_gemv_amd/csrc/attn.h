@@ -40,8 +40,8 @@ struct SharedArgs : AttnArgs {
     const int32_t *starts, *shared;
     int n_groups, max_shared, max_own;
     int prefix_tiles, prefix_chunks, slots;   // tiles of a chunk of shared tokens; chunks
-    int row_tiles, wide;                      // tiles of query rows; 128 rows each, else 32
-    int seq0, tile0;                          // first sequence, first row tile of this launch
+    int row_tiles, wide;                      // tiles of query rows, at most; 128 rows each, else 32
+    int seq0, group0;                         // first sequence, first row of workgroups of this launch
 };
 
 // One partial result: the running maximum and sum, then head_dim outputs.

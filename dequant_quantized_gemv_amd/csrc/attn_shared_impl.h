@@ -23,8 +23,8 @@
 // Scores as in the decode kernel: exact keys, q in two fp16 parts.  The low
 // part is never 0 beside a high part that is not, so that a key which
 // overflowed to infinity keeps its sign.  Probabilities: with 8-bit values
-// all 24 bits in three bf16 parts; with fp16 values two fp16 parts of 2^15 p,
-// which holds p within 2^-21 of itself and 2^-39 of the row's largest (the exact form,
+// all 24 bits in three bf16 parts; with fp16 values two fp16 parts of 2^12 p,
+// which holds p within 2^-21 of itself and 2^-36 of the row's largest (the exact form,
 // v_mfma_f32_16x16x4_f32, has an eighth of the rate, and this kernel is bound
 // by its products).
 #pragma once
@@ -55,6 +55,18 @@ __device__ __forceinline__ float pair_sum(float v) {
     return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
 }
 
+// High and low fp16 parts of eight values: the high one rounded toward zero, the
+// low one the rounded difference (one mixed-precision fma makes it; minus is -1,
+// held where the compiler does not know it and make a subtraction of it).
+__device__ __forceinline__ void split8_mixed(const float (&p)[8], float minus, h8_t &hi, h8_t &lo) {
+    u4_t h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(p[2 * i], p[2 * i + 1]));
+    hi = __builtin_bit_cast(h8_t, h);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) lo[i] = (_Float16)__builtin_fmaf((float)hi[i], minus, p[i]);
+}
+
 template <int D, bool I8, bool WIDE>
 __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prefix_kernel(const SharedArgs a) {
     constexpr int ROWS = prefix_rows(WIDE), BN = prefix_tokens(WIDE);
@@ -76,48 +88,55 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prefix_kernel(cons
     const int wn = WIDE ? 0 : wave, row0 = WIDE ? 32 * wave : 0;
 
     // The row tiles of one chunk and head are neighbours on one XCD, whose L2
-    // then has the chunk's rows for all of them but the first.
+    // then has the chunk's rows for all of them but the first.  How many row tiles
+    // there are is known here only: workgroups without one come last (among the
+    // others they left CUs with half of their work: 148 -> 121 us for 64 x 32768).
     const int units = a.n_kv * a.prefix_chunks;
-    const int x = blockIdx.x & 7, y = blockIdx.x >> 3;
-    const int unit = y / a.row_tiles * 8 + x;
+    int at = 0, n = 0, sh = 0, tiles = 0, upto = 0;   // a lane's group, 64 groups at a time
+    auto groups_from = [&](int g0) __attribute__((always_inline)) {
+        const int gi = g0 + lane;
+        at = n = sh = 0;
+        if (gi < a.n_groups) {
+            at = min(max(a.starts[gi], 0), a.n_seqs);
+            n = (min(max(a.starts[gi + 1], at), a.n_seqs) - at) * a.group;
+            sh = a.shared[gi];
+        }
+        upto = tiles = (n + ROWS - 1) / ROWS;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int u = __shfl_up(upto, d);
+            if (lane >= d) upto += u;
+        }
+    };
+    int total = 0;
+    for (int g0 = 0; g0 < a.n_groups; g0 += 64) {
+        groups_from(g0);
+        total += __builtin_amdgcn_readlane(upto, 63);
+    }
+    // (groups out of order may add up to anything; their rows are NaN in the end)
+    if (total <= 0 || total > a.row_tiles) return;
+    const int nth = (int)(blockIdx.x >> 3) + a.group0;
+    const int unit = nth / total * 8 + (int)(blockIdx.x & 7);
     if (unit >= units) return;
     const int kvh = unit % a.n_kv, chunk = unit / a.n_kv;
-    int tile = y % a.row_tiles + a.tile0;
+    int tile = nth % total;
 
     // the group that the row tile is of
     int first = 0, rows = 0, shared = 0;
-    {
-        bool is = false;
-        for (int g0 = 0; g0 < a.n_groups && !is; g0 += 64) {
-            const int gi = g0 + lane;
-            int at = 0, n = 0, sh = 0;
-            if (gi < a.n_groups) {
-                at = min(max(a.starts[gi], 0), a.n_seqs);
-                n = (min(max(a.starts[gi + 1], at), a.n_seqs) - at) * a.group;
-                sh = a.shared[gi];
-            }
-            const int tiles = (n + ROWS - 1) / ROWS;
-            int upto = tiles;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int u = __shfl_up(upto, d);
-                if (lane >= d) upto += u;
-            }
-            const uint64_t past = __ballot(upto > tile);
-            if (past != 0) {
-                const int src = __builtin_ctzll(past);
-                first = __builtin_amdgcn_readlane(at, src);
-                rows = __builtin_amdgcn_readlane(n, src);
-                shared = __builtin_amdgcn_readlane(sh, src);
-                tile -= __builtin_amdgcn_readlane(upto, src) - __builtin_amdgcn_readlane(tiles, src);
-                is = true;
-            } else {
-                tile -= __builtin_amdgcn_readlane(upto, 63);
-            }
+    for (int g0 = 0; g0 < a.n_groups; g0 += 64) {
+        if (a.n_groups > 64) groups_from(g0);
+        const uint64_t past = __ballot(upto > tile);
+        if (past != 0) {
+            const int src = __builtin_ctzll(past);
+            first = __builtin_amdgcn_readlane(at, src);
+            rows = __builtin_amdgcn_readlane(n, src);
+            shared = __builtin_amdgcn_readlane(sh, src);
+            tile -= __builtin_amdgcn_readlane(upto, src) - __builtin_amdgcn_readlane(tiles, src);
+            break;
         }
-        // (a tile that is not there, and whatever groups out of order lead to)
-        if (!is || tile < 0 || (int64_t)tile * ROWS >= rows) return;
+        tile -= __builtin_amdgcn_readlane(upto, 63);
     }
+    if (tile < 0 || (int64_t)tile * ROWS >= rows) return;
     if (shared <= 0 || shared > a.max_shared) return;
     const int64_t chunk_tokens = (int64_t)a.prefix_tiles * BN;
     if (chunk * chunk_tokens >= shared) return;
@@ -253,14 +272,21 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prefix_kernel(cons
         }
         if constexpr (I8) qexp += 9;  // codes are held times 2^-9
     }
+    // (where 2^qexp is no normal number, all scores are 0 to the last bit either way)
+    const float back = ldexpf(1.0f, max(qexp, -126));
 
-    constexpr float LIFT = I8 ? 0.0f : 15.0f;   // probabilities are held times 2^LIFT
+    // Probabilities are held times 2^LIFT, and the maximum that they are relative
+    // to follows the largest score only where that is past it by SLACK (2^15 is what
+    // fp16 has room for): rows of one wave seldom rise together.
+    constexpr float LIFT = I8 ? 0.0f : 12.0f, SLACK = 3.0f;
     f16_t o[DB];
 #pragma unroll
     for (int c = 0; c < DB; ++c)
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[c][r] = 0.0f;
     float m = kAttnLow, l = 0.0f;               // m: the running maximum less LIFT
+    float minus = -1.0f;
+    asm("" : "+s"(minus));
 
     for (int n = 0; n < ntiles; ++n) {
         __syncthreads();   // (the last tile and its places are read)
@@ -293,21 +319,21 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prefix_kernel(cons
                 c = __builtin_amdgcn_mfma_f32_32x32x16_f16(kk, ql[s], c, 0, 0, 0);
             }
             float p[16];
-            float top = kAttnLow;
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                p[r] = ldexpf(c[r], qexp);
+                p[r] = c[r];
                 if constexpr (I8) p[r] *= scales[b0 + 8 * (r >> 2) + 4 * g + (r & 3)];
             }
             if (here < 32) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    if (8 * (r >> 2) + 4 * g + (r & 3) >= here) p[r] = kAttnLow;
+                    if (8 * (r >> 2) + 4 * g + (r & 3) >= here) p[r] = -__builtin_inff();
             }
+            float top = p[0];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) top = fmaxf(top, p[r]);
-            top = pair_max(top) - LIFT;
-            if (__any(top > m)) {
+            for (int r = 1; r < 16; ++r) top = __builtin_elementwise_maximum(top, p[r]);
+            top = __builtin_fmaf(pair_max(top), back, -LIFT);
+            if (__any(top > m + SLACK)) {
                 const float mn = fmaxf(m, top);
                 const float f = __builtin_amdgcn_exp2f(m - mn);
                 l *= f;
@@ -319,8 +345,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prefix_kernel(cons
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                p[r] = __builtin_amdgcn_exp2f(p[r] - m);
-                if (here < 32 && 8 * (r >> 2) + 4 * g + (r & 3) >= here) p[r] = 0.0f;
+                p[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[r], back, -m));
                 l += p[r];
             }
 #pragma unroll
@@ -346,7 +371,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prefix_kernel(cons
                     }
                 } else {
                     h8_t hi, lo;
-                    split8(ps, hi, lo);
+                    split8_mixed(ps, minus, hi, lo);
 #pragma unroll
                     for (int c2 = 0; c2 < DB; ++c2) {
                         const h8_t vv = *reinterpret_cast<const h8_t *>(at + 32 * c2 * L::kDim);
@@ -509,13 +534,12 @@ int attn_prefix_launch(const SharedArgs &a, hipStream_t stream) {
     if (bytes > 65536 && hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)bytes) != hipSuccess)
         return QK_ERR_LAUNCH;
-    const int64_t units = ((int64_t)a.n_kv * a.prefix_chunks + 7) / 8 * 8;
-    const int64_t most = max_groups(256) / units;  // row tiles of one launch
-    for (int64_t tile = 0; tile < a.row_tiles; tile += most) {
+    // rows of workgroups, one for each XCD
+    const int64_t all = ((int64_t)a.n_kv * a.prefix_chunks + 7) / 8 * a.row_tiles, most = max_groups(256) / 8;
+    for (int64_t i = 0; i < all; i += most) {
         SharedArgs p = a;
-        p.tile0 = (int)tile;
-        p.row_tiles = (int)std::min<int64_t>(a.row_tiles - tile, most);
-        const int st = launch_lds(kern, dim3((unsigned)(units * p.row_tiles)), dim3(256), bytes, stream, p);
+        p.group0 = (int)i;
+        const int st = launch_lds(kern, dim3((unsigned)(8 * std::min(all - i, most))), dim3(256), bytes, stream, p);
         if (st != QK_OK) return st;
     }
     return QK_OK;

@@ -551,7 +551,7 @@ size_t qk_attn_decode_workspace(const qk_kv_cache *cache, int64_t n_seqs, int64_
  * which anything arrives; n_seqs, n_groups, max_shared and max_own decide the
  * order of its sums.
  * Scores as in qk_attn_decode.  Probabilities meet fp16 values in two fp16
- * parts: within 2^-21 of themselves and 2^-39 of the row's largest; 8-bit
+ * parts: within 2^-21 of themselves and 2^-36 of the row's largest; 8-bit
  * values with all their 24 bits.  An fp16 value that overflowed to infinity may
  * give NaN.
  *

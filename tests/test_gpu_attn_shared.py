@@ -6,7 +6,7 @@ Tolerance as of the decode attention (tests/test_gpu_attn.py), with A = sum_t p_
   scores: 2^-21 (Z + scale * log2(e) * max|q| * sum|K|) + (D + 4) u Z in log2, ln2 of
   which is relative in p; p itself 2^-22 (exponential, scales) and 2^-21 (its
   parts); numerator and denominator: twice, and T sums (T u each), 8 u to join.
-  fp16 values meet p in parts that stop at 2^-39 of the largest p: 2^-39 sum_t |V_t|
+  fp16 values meet p in parts that stop at 2^-36 of the largest p: 2^-36 sum_t |V_t|
   / sum_t p_t besides.
   Below fp32's range nothing is held: 2^-126 sum_t |V_t|.
 """
@@ -129,7 +129,7 @@ class Batch:
                 sv = np.abs(V).sum(0)
                 tol[s, rows] = (2 * (np.log(2) * dz + 2.0 ** -22 + 2.0 ** -21) + 2 * len(K) * U + 8 * U) * A + 2.0 ** -126 * sv
                 if self.kind == "f16":
-                    tol[s, rows] += 2.0 ** -39 * sv / total
+                    tol[s, rows] += 2.0 ** -36 * sv / total
         return y, tol
 
     def run(self, scale=None, out="f32", bounds=None, fill=0xA5):
