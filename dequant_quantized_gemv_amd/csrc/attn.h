@@ -41,7 +41,8 @@ struct SharedArgs : AttnArgs {
     int n_groups, max_shared, max_own;
     int prefix_tiles, prefix_chunks, slots;   // tiles of a chunk of shared tokens; chunks
     int row_tiles, wide;                      // tiles of query rows, at most; 128 rows each, else 32
-    int seq0, group0;                         // first sequence, first row of workgroups of this launch
+    int seq0, group0;                         // first sequence, first eight of workgroups of this launch
+    int own_blocks;                           // workgroups of sequences' own tokens in it
 };
 
 // One partial result: the running maximum and sum, then head_dim outputs.

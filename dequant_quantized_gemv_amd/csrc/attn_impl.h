@@ -159,17 +159,19 @@ __device__ __forceinline__ int shared_tokens(const SharedArgs &a, int seq, int l
 // scales) of the tile's token l % 32, and lanes take them from one another.
 // With SharedArgs the tokens that a sequence has of its own, behind those that
 // its group shares, always to partial results.
-template <int D, bool I8, bool TILED, class ARGS = AttnArgs>
-__global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode_kernel(const ARGS a) {
+// A workgroup's results on the way to one another: maximum and sum, outputs.
+typedef float AttnWaveSums[kAttnWaves][kAttnHeads][2];
+template <int D> using AttnWaveOutputs = float[kAttnWaves][kAttnHeads][D + 4];
+
+// Workgroup `block` of `blocks`.
+template <int D, bool I8, bool TILED, class ARGS>
+__device__ __forceinline__ void attn_decode_block(const ARGS &a, const int block, const int blocks, AttnWaveSums &sm, AttnWaveOutputs<D> &so) {
     constexpr bool SHARED = std::is_same_v<ARGS, SharedArgs>;
     constexpr int ES = I8 ? 1 : 2;         // bytes of a key or value element
     constexpr int STEPS = D / 32;          // products over the head dimension
     constexpr int DPL = D / 16;            // dims of a lane's V row piece = tiles of O^T
     constexpr int VB = DPL * ES;           // its bytes
     constexpr int KP = I8 ? (STEPS + 1) / 2 : STEPS;  // 16-byte pieces of a lane's K row part
-    __shared__ float sm[kAttnWaves][kAttnHeads][2];
-    __shared__ __attribute__((aligned(16))) float so[kAttnWaves][kAttnHeads][D + 4];
-
     typedef const __attribute__((address_space(4))) int32_t cint_t;  // scalar loads
 
     const int lane = threadIdx.x & 63;
@@ -178,8 +180,8 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
     // Chunks outermost: workgroups go round the XCDs in turn, so with chunks
     // innermost the chunks that only long sequences have would meet on the
     // same XCDs; and a sequence's first chunks, which are whole, start first.
-    int b = blockIdx.x;
-    const int rows = gridDim.x / a.nchunks;
+    int b = block;
+    const int rows = blocks / a.nchunks;
     const int chunk = b / rows;
     b -= chunk * rows;
     const int ht = b % a.head_tiles;
@@ -582,6 +584,13 @@ __global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode
             *reinterpret_cast<f4_t *>(part + 4 + d) = acc;
         }
     }
+}
+
+template <int D, bool I8, bool TILED>
+__global__ __launch_bounds__(64 * kAttnWaves, D <= 128 ? 2 : 1) void attn_decode_kernel(const AttnArgs a) {
+    __shared__ AttnWaveSums sm;
+    __shared__ __attribute__((aligned(16))) AttnWaveOutputs<D> so;
+    attn_decode_block<D, I8, TILED>(a, blockIdx.x, gridDim.x, sm, so);
 }
 
 // Joins the chunks of one (sequence, head): a workgroup's threads take the

@@ -1,13 +1,13 @@
 // attn_shared_impl.h - attention of one new token per sequence where groups of
 // sequences share their first tokens (gfx950): those are read once per group.
 //
-// Three launches.  The prefix kernel takes the shared tokens for all query
-// rows of a group (every sequence's heads that share a key-value head: a
-// matrix product instead of a product per row), the decode kernel takes each
-// sequence's own tokens, and both leave partial results (running maximum, sum
-// and output) that the join combines.
+// Two launches.  In the first, some workgroups take the shared tokens for all
+// query rows of a group (every sequence's heads that share a key-value head: a
+// matrix product instead of a product per row) and others each sequence's own
+// tokens as the decode kernel does; both leave partial results (running maximum,
+// sum and output) that the join combines.
 //
-// Prefix kernel: a workgroup of four waves takes a tile of query rows over one
+// Shared tokens: a workgroup of four waves takes a tile of query rows over one
 // chunk of the shared tokens.  Keys and values go through LDS in tiles, keys
 // as they are and values transposed, so that both products read their operands
 // 16 bytes at a time, and v_mfma_f32_32x32x16 takes 32 rows per wave:
@@ -68,7 +68,7 @@ __device__ __forceinline__ void split8_mixed(const float (&p)[8], float minus, h
 }
 
 template <int D, bool I8, bool WIDE>
-__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prefix_kernel(const SharedArgs a) {
+__device__ __forceinline__ void attn_prefix_block(const SharedArgs &a, const int block, uint8_t *lds) {
     constexpr int ROWS = prefix_rows(WIDE), BN = prefix_tokens(WIDE);
     constexpr int WN = 128 / ROWS;             // waves that take different tokens of the same rows
     constexpr int SUBS = BN / WN / 32;         // 32-token blocks of a wave
@@ -78,7 +78,6 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prefix_kernel(cons
     constexpr int UNITS = NQ * (D / 8);        // four tokens by eight dims each
     constexpr int NU = (UNITS + 255) / 256;    // of a thread
     using L = PrefixLds<D, BN>;
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     int64_t *places = reinterpret_cast<int64_t *>(lds + L::kPlaces);
     float *scales = reinterpret_cast<float *>(lds + L::kScales);
 
@@ -115,8 +114,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prefix_kernel(cons
     }
     // (groups out of order may add up to anything; their rows are NaN in the end)
     if (total <= 0 || total > a.row_tiles) return;
-    const int nth = (int)(blockIdx.x >> 3) + a.group0;
-    const int unit = nth / total * 8 + (int)(blockIdx.x & 7);
+    const int nth = (block >> 3) + a.group0;
+    const int unit = nth / total * 8 + (block & 7);
     if (unit >= units) return;
     const int kvh = unit % a.n_kv, chunk = unit / a.n_kv;
     int tile = nth % total;
@@ -438,6 +437,22 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_prefix_kernel(cons
                 f4_t{o[c][4 * r], o[c][4 * r + 1], o[c][4 * r + 2], o[c][4 * r + 3]};
 }
 
+// One launch for both: own tokens (bound by memory, of uneven lengths) first,
+// so that the shared ones fill the CUs as those end.
+template <int D, bool I8, bool TILED, bool WIDE>
+__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_shared_kernel(const SharedArgs a) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    if ((int)blockIdx.x < a.own_blocks) {
+        auto &sm = *reinterpret_cast<AttnWaveSums *>(lds);
+        auto &so = *reinterpret_cast<AttnWaveOutputs<D> *>(lds + sizeof(AttnWaveSums));
+        attn_decode_block<D, I8, TILED>(a, blockIdx.x, a.own_blocks, sm, so);
+    } else {
+        // (a multiple of 8 behind the own tokens' workgroups, for the XCDs)
+        const int block = (int)blockIdx.x - (a.own_blocks + 7) / 8 * 8;
+        if (block >= 0) attn_prefix_block<D, I8, WIDE>(a, block, lds);
+    }
+}
+
 // Joins the partial results of one (sequence, head): those of the shared
 // tokens' chunks, then those of its own.
 template <int D>
@@ -527,38 +542,39 @@ __global__ __launch_bounds__(256) void attn_shared_join_kernel(const SharedArgs 
     }
 }
 
-template <int D, bool I8, bool WIDE>
-int attn_prefix_launch(const SharedArgs &a, hipStream_t stream) {
-    constexpr size_t bytes = PrefixLds<D, prefix_tokens(WIDE)>::kBytes;
-    const auto kern = attn_prefix_kernel<D, I8, WIDE>;
+template <int D, bool I8, bool TILED, bool WIDE>
+int attn_shared_start(const SharedArgs &a, hipStream_t stream) {
+    constexpr size_t bytes = std::max<size_t>(PrefixLds<D, prefix_tokens(WIDE)>::kBytes, sizeof(AttnWaveSums) + sizeof(AttnWaveOutputs<D>));
+    const auto kern = attn_shared_kernel<D, I8, TILED, WIDE>;
     if (bytes > 65536 && hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)bytes) != hipSuccess)
         return QK_ERR_LAUNCH;
-    // rows of workgroups, one for each XCD
-    const int64_t all = ((int64_t)a.n_kv * a.prefix_chunks + 7) / 8 * a.row_tiles, most = max_groups(256) / 8;
-    for (int64_t i = 0; i < all; i += most) {
+    // workgroups of the shared tokens in eights, one for each XCD, and of a sequence's own
+    const int64_t eights = a.prefix_chunks > 0 ? ((int64_t)a.n_kv * a.prefix_chunks + 7) / 8 * a.row_tiles : 0;
+    const int64_t each = (int64_t)a.n_kv * a.head_tiles * a.nchunks, most = max_groups(256) / 8 * 8;
+    auto go = [&](int64_t seq, int64_t n, int64_t eight, int64_t ne) {
         SharedArgs p = a;
-        p.group0 = (int)i;
-        const int st = launch_lds(kern, dim3((unsigned)(8 * std::min(all - i, most))), dim3(256), bytes, stream, p);
-        if (st != QK_OK) return st;
-    }
-    return QK_OK;
+        p.seq0 = (int)seq;
+        p.own_blocks = (int)(n * each);
+        p.group0 = (int)eight;
+        return launch_lds(kern, dim3((unsigned)((n * each + 7) / 8 * 8 + 8 * ne)), dim3(256), bytes, stream, p);
+    };
+    if (a.n_seqs * each <= most - 8 * eights) return go(0, a.n_seqs, 0, eights);
+    int st = QK_OK;
+    for (int64_t i = 0; i < eights && st == QK_OK; i += most / 8) st = go(0, 0, i, std::min(eights - i, most / 8));
+    for (int64_t i = 0; i < a.n_seqs && st == QK_OK; i += most / each) st = go(i, std::min<int64_t>(a.n_seqs - i, most / each), 0, 0);
+    return st;
 }
 
 template <int D, bool I8>
 int attn_shared_dim(const SharedArgs &a, bool tiled, hipStream_t stream) {
-    int st = QK_OK;
-    if (a.prefix_chunks > 0) st = a.wide ? attn_prefix_launch<D, I8, true>(a, stream) : attn_prefix_launch<D, I8, false>(a, stream);
-    const int64_t rows = (int64_t)a.n_kv * a.head_tiles * a.nchunks;
-    const int64_t most = std::max<int64_t>(1, max_groups(256) / std::max<int64_t>(rows, a.n_heads));  // sequences of one launch
-    for (int64_t seq = 0; seq < a.n_seqs && st == QK_OK; seq += most) {
+    int st = tiled ? (a.wide ? attn_shared_start<D, I8, true, true>(a, stream) : attn_shared_start<D, I8, true, false>(a, stream))
+                   : (a.wide ? attn_shared_start<D, I8, false, true>(a, stream) : attn_shared_start<D, I8, false, false>(a, stream));
+    const int64_t most = max_groups(256) / a.n_heads;  // sequences of one launch
+    for (int64_t i = 0; i < a.n_seqs && st == QK_OK; i += most) {
         SharedArgs p = a;
-        p.seq0 = (int)seq;
-        const int64_t n = std::min<int64_t>(a.n_seqs - seq, most);
-        const dim3 grid((unsigned)(n * rows)), block(64 * kAttnWaves);
-        st = tiled ? launch(attn_decode_kernel<D, I8, true, SharedArgs>, grid, block, stream, p)
-                   : launch(attn_decode_kernel<D, I8, false, SharedArgs>, grid, block, stream, p);
-        if (st == QK_OK) st = launch(attn_shared_join_kernel<D>, dim3((unsigned)(n * a.n_heads)), dim3(256), stream, p);
+        p.seq0 = (int)i;
+        st = launch(attn_shared_join_kernel<D>, dim3((unsigned)(std::min<int64_t>(a.n_seqs - i, most) * a.n_heads)), dim3(256), stream, p);
     }
     return st;
 }
