@@ -257,8 +257,8 @@ bool attn_fill(const qk_kv_cache &c, qk::AttnArgs &a, const float *q, int64_t q_
     return c.page_size % 16 == 0 && a.slot_stride < (int64_t(1) << 26) && (!i8 || c.scale_slot_stride == 1);
 }
 
-// Sizes and splits of an attention with shared first tokens.  Rows of 32 where
-// the groups have no more than that many query rows on average, else of 128.
+// Sizes and splits of an attention with shared first tokens: tiles of 64 query
+// rows where the groups have no more than that on average, else of 128.
 int shared_plan(const qk_kv_cache &c, int64_t n_seqs, int64_t n_q_heads, int64_t n_groups, int64_t max_len,
                 int64_t max_shared, int64_t max_own, qk::SharedArgs &a) {
     if (n_groups < 0 || n_groups > kMaxDim || max_shared < 0 || max_own < 1 || max_len < 1 || max_len > (int64_t(1) << 30) ||
@@ -277,8 +277,8 @@ int shared_plan(const qk_kv_cache &c, int64_t n_seqs, int64_t n_q_heads, int64_t
     if (n_groups > 0 && max_shared > 0) {
         const int64_t groups = std::min(n_groups, n_seqs);
         const int64_t each = (n_seqs * a.group + groups - 1) / groups;   // query rows of a group
-        a.wide = each > 32;
-        const int64_t rows = qk::prefix_rows(a.wide), tokens = qk::prefix_tokens(a.wide);
+        a.row_waves = each > 64 ? 4 : 2;
+        const int64_t rows = qk::prefix_rows(a.row_waves), tokens = qk::kPrefixTokens;
         // row tiles at most, and about as many as there will be
         a.row_tiles = (int)(n_seqs * a.group / rows + groups);
         const int64_t about = groups * ((each + rows - 1) / rows);
@@ -302,7 +302,7 @@ size_t shared_workspace(const qk_kv_cache &c, const qk::SharedArgs &a) {
 size_t shared_workspace_bound(const qk_kv_cache &c, const qk::SharedArgs &a) {
     const int64_t target = attn_target(c), seqs = a.n_seqs, heads = a.n_heads;
     int64_t parts = 0;
-    if (a.max_shared > 0) parts = std::min(seqs * heads * ((a.max_shared + 63) / 64), seqs * heads + target * qk::prefix_rows(1));
+    if (a.max_shared > 0) parts = std::min(seqs * heads * ((a.max_shared + qk::kPrefixTokens - 1) / qk::kPrefixTokens), seqs * heads + target * qk::prefix_rows(4));
     const int64_t tiles = ((int64_t)a.max_own + 2 * qk::kAttnTile - 2) / qk::kAttnTile, row = (int64_t)a.n_kv * a.head_tiles;
     parts += heads * std::min(seqs * ((tiles + qk::kAttnWaves - 1) / qk::kAttnWaves), target / row + seqs);
     return 4 * (size_t)parts * (size_t)qk::attn_part_floats((int)c.head_dim);

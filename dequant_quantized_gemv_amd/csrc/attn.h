@@ -40,7 +40,7 @@ struct SharedArgs : AttnArgs {
     const int32_t *starts, *shared;
     int n_groups, max_shared, max_own;
     int prefix_tiles, prefix_chunks, slots;   // tiles of a chunk of shared tokens; chunks
-    int row_tiles, wide;                      // tiles of query rows, at most; 128 rows each, else 32
+    int row_tiles, row_waves;                 // tiles of query rows, at most; waves with rows of their own in each
     int seq0, group0;                         // first sequence, first eight of workgroups of this launch
     int own_blocks;                           // workgroups of sequences' own tokens in it
 };
@@ -74,9 +74,10 @@ __host__ __device__ inline AttnSpan own_span(int len, int shared) {
     return AttnSpan{len, shared, start, 0, (len - start + kAttnTile - 1) / kAttnTile};
 }
 
-// Query rows of a tile and tokens of a tile of the shared tokens' kernel.
-constexpr int prefix_rows(int wide) { return wide ? 128 : 32; }
-constexpr int prefix_tokens(int wide) { return wide ? 64 : 128; }
+// Tokens of a tile of the shared ones, and query rows of one: `row_waves` (2 or
+// 4) of a workgroup's waves have rows of their own.
+constexpr int kPrefixTokens = 64;
+constexpr int prefix_rows(int row_waves) { return 32 * row_waves; }
 
 struct StoreArgs {
     uint8_t *kc, *vc;

@@ -17,8 +17,11 @@
 // one g in a lane, and since their order is free as long as both operands have
 // the same, the values' tokens are stored in the order that the results have.
 // The next tile's rows are in registers while one is worked on.
-// 128 rows (every wave all tokens of a tile of 64) or, where a group has few,
-// 32 (every wave a quarter of the tokens of 128, joined in LDS at the end).
+// A workgroup has 128 rows, every wave all tokens of a tile, or, where groups
+// have no more, 64, the waves in two halves with half of the tokens each, joined in
+// LDS at the end: half as many partial results per row (8 rows of 32768 tokens
+// 44.3 / 45.8 us with 64 / 128, 64 rows 114 / 102; 32 rows and a tile of 128 tokens
+// lost to both: 59).
 //
 // Scores as in the decode kernel: exact keys, q in two fp16 parts.  The low
 // part is never 0 beside a high part that is not, so that a key which
@@ -35,8 +38,9 @@ namespace qk {
 
 typedef float f16_t __attribute__((ext_vector_type(16)));
 
-template <int D, int BN>
+template <int D>
 struct PrefixLds {
+    static constexpr int BN = kPrefixTokens;
     static constexpr int kRow = 2 * D + 16;    // bytes of a key row (the 16 keep 16-byte reads of 16 rows off each other's banks)
     static constexpr int kDim = 2 * BN + 16;   // bytes of a dimension's values
     static constexpr int kValues = BN * kRow;
@@ -67,24 +71,24 @@ __device__ __forceinline__ void split8_mixed(const float (&p)[8], float minus, h
     for (int i = 0; i < 8; ++i) lo[i] = (_Float16)__builtin_fmaf((float)hi[i], minus, p[i]);
 }
 
-template <int D, bool I8, bool WIDE>
+template <int D, bool I8, int WM>
 __device__ __forceinline__ void attn_prefix_block(const SharedArgs &a, const int block, uint8_t *lds) {
-    constexpr int ROWS = prefix_rows(WIDE), BN = prefix_tokens(WIDE);
-    constexpr int WN = 128 / ROWS;             // waves that take different tokens of the same rows
+    constexpr int ROWS = prefix_rows(WM), BN = kPrefixTokens;
+    constexpr int WN = 4 / WM;                 // waves that take different tokens of the same rows
     constexpr int SUBS = BN / WN / 32;         // 32-token blocks of a wave
     constexpr int ES = I8 ? 1 : 2;
     constexpr int KS = D / 16, DB = D / 32;    // steps of the first product; blocks of output dims
     constexpr int NQ = BN / 4;                 // quads of tokens
     constexpr int UNITS = NQ * (D / 8);        // four tokens by eight dims each
     constexpr int NU = (UNITS + 255) / 256;    // of a thread
-    using L = PrefixLds<D, BN>;
+    using L = PrefixLds<D>;
     int64_t *places = reinterpret_cast<int64_t *>(lds + L::kPlaces);
     float *scales = reinterpret_cast<float *>(lds + L::kScales);
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 5, j = lane & 31;
-    const int wn = WIDE ? 0 : wave, row0 = WIDE ? 32 * wave : 0;
+    const int wn = wave / WM, row0 = 32 * (wave % WM);
 
     // The row tiles of one chunk and head are neighbours on one XCD, whose L2
     // then has the chunk's rows for all of them but the first.  How many row tiles
@@ -308,15 +312,26 @@ __device__ __forceinline__ void attn_prefix_block(const SharedArgs &a, const int
             const int b0 = (SUBS * wn + sub) * 32;   // the block's first token in the tile
             const int here = t1 - t0 - n * BN - b0;  // tokens from there on
             if (here <= 0) continue;
+            // all operands of a product are asked for before its first instruction
+            h8_t kk[KS];
+#pragma unroll
+            for (int s = 0; s < KS; ++s) kk[s] = *reinterpret_cast<const h8_t *>(lds + (b0 + j) * L::kRow + 32 * s + 16 * g);
+            __builtin_amdgcn_sched_barrier(0);
             f16_t c;
 #pragma unroll
             for (int r = 0; r < 16; ++r) c[r] = 0.0f;
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                const h8_t kk = *reinterpret_cast<const h8_t *>(lds + (b0 + j) * L::kRow + 32 * s + 16 * g);
-                c = __builtin_amdgcn_mfma_f32_32x32x16_f16(kk, qh[s], c, 0, 0, 0);
-                c = __builtin_amdgcn_mfma_f32_32x32x16_f16(kk, ql[s], c, 0, 0, 0);
+                c = __builtin_amdgcn_mfma_f32_32x32x16_f16(kk[s], qh[s], c, 0, 0, 0);
+                c = __builtin_amdgcn_mfma_f32_32x32x16_f16(kk[s], ql[s], c, 0, 0, 0);
             }
+            u4_t vv[2][DB];
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int c2 = 0; c2 < DB; ++c2)
+                    vv[s][c2] = *reinterpret_cast<const u4_t *>(lds + L::kValues + (32 * c2 + j) * L::kDim + 2 * (b0 + 16 * s + 8 * g));
+            __builtin_amdgcn_sched_barrier(0);
             float p[16];
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
@@ -352,7 +367,6 @@ __device__ __forceinline__ void attn_prefix_block(const SharedArgs &a, const int
                 float ps[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) ps[i] = p[8 * s + i];
-                const uint8_t *at = lds + L::kValues + j * L::kDim + 2 * (b0 + 16 * s + 8 * g);
                 if constexpr (I8) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -364,18 +378,18 @@ __device__ __forceinline__ void attn_prefix_block(const SharedArgs &a, const int
                     split8_bf16(ps, part);
 #pragma unroll
                     for (int c2 = 0; c2 < DB; ++c2) {
-                        const b8_t vv = *reinterpret_cast<const b8_t *>(at + 32 * c2 * L::kDim);
+                        const b8_t w = __builtin_bit_cast(b8_t, vv[s][c2]);
 #pragma unroll
-                        for (int e = 0; e < 3; ++e) o[c2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vv, part[e], o[c2], 0, 0, 0);
+                        for (int e = 0; e < 3; ++e) o[c2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, part[e], o[c2], 0, 0, 0);
                     }
                 } else {
                     h8_t hi, lo;
                     split8_mixed(ps, minus, hi, lo);
 #pragma unroll
                     for (int c2 = 0; c2 < DB; ++c2) {
-                        const h8_t vv = *reinterpret_cast<const h8_t *>(at + 32 * c2 * L::kDim);
-                        o[c2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv, hi, o[c2], 0, 0, 0);
-                        o[c2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv, lo, o[c2], 0, 0, 0);
+                        const h8_t w = __builtin_bit_cast(h8_t, vv[s][c2]);
+                        o[c2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(w, hi, o[c2], 0, 0, 0);
+                        o[c2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(w, lo, o[c2], 0, 0, 0);
                     }
                 }
             }
@@ -384,12 +398,13 @@ __device__ __forceinline__ void attn_prefix_block(const SharedArgs &a, const int
     l = pair_sum(l);
     if (__syncthreads_or(bad)) l = __builtin_nanf("");
 
-    if constexpr (!WIDE) {
-        // the waves' results, the first one's registers taking them all
+    if constexpr (WN > 1) {
+        // the results of waves with the same rows, the first one's registers taking them all
         float *other = reinterpret_cast<float *>(lds);
         constexpr int PER = (16 * DB + 2) * 64;
-        if (wave > 0) {
-            float *mine = other + (wave - 1) * PER;
+        static_assert(4 * PER * (4 - WM) <= L::kPlaces, "waves' results in the tile's place");
+        if (wn > 0) {
+            float *mine = other + (wave - WM) * PER;
 #pragma unroll
             for (int c = 0; c < DB; ++c)
 #pragma unroll
@@ -398,11 +413,11 @@ __device__ __forceinline__ void attn_prefix_block(const SharedArgs &a, const int
             mine[(16 * DB + 1) * 64 + lane] = l;
         }
         __syncthreads();
-        if (wave > 0) return;
+        if (wn > 0) return;
         float ms[WN], mm = m;
 #pragma unroll
         for (int w = 1; w < WN; ++w) {
-            ms[w] = other[(w - 1) * PER + 16 * DB * 64 + lane];
+            ms[w] = other[((w - 1) * WM + wave) * PER + 16 * DB * 64 + lane];
             mm = fmaxf(mm, ms[w]);
         }
         const float f0 = __builtin_amdgcn_exp2f(m - mm);
@@ -414,7 +429,7 @@ __device__ __forceinline__ void attn_prefix_block(const SharedArgs &a, const int
 #pragma unroll
         for (int w = 1; w < WN; ++w) {
             const float f = __builtin_amdgcn_exp2f(ms[w] - mm);
-            const float *from = other + (w - 1) * PER + lane;
+            const float *from = other + ((w - 1) * WM + wave) * PER + lane;
             l += f * from[(16 * DB + 1) * 64];
 #pragma unroll
             for (int c = 0; c < DB; ++c)
@@ -439,7 +454,7 @@ __device__ __forceinline__ void attn_prefix_block(const SharedArgs &a, const int
 
 // One launch for both: own tokens (bound by memory, of uneven lengths) first,
 // so that the shared ones fill the CUs as those end.
-template <int D, bool I8, bool TILED, bool WIDE>
+template <int D, bool I8, bool TILED, int WM>
 __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_shared_kernel(const SharedArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     if ((int)blockIdx.x < a.own_blocks) {
@@ -449,7 +464,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_shared_kernel(cons
     } else {
         // (a multiple of 8 behind the own tokens' workgroups, for the XCDs)
         const int block = (int)blockIdx.x - (a.own_blocks + 7) / 8 * 8;
-        if (block >= 0) attn_prefix_block<D, I8, WIDE>(a, block, lds);
+        if (block >= 0) attn_prefix_block<D, I8, WM>(a, block, lds);
     }
 }
 
@@ -477,7 +492,7 @@ __global__ __launch_bounds__(256) void attn_shared_join_kernel(const SharedArgs 
     const int row = threadIdx.x / COLS, col = threadIdx.x % COLS;
     int n1 = 0, n = 0;
     if (fine) {
-        const int64_t chunk = (int64_t)a.prefix_tiles * prefix_tokens(a.wide);
+        const int64_t chunk = (int64_t)a.prefix_tiles * kPrefixTokens;
         n1 = shared > 0 ? (int)((shared + chunk - 1) / chunk) : 0;
         n = n1 + (len > shared ? (own_span(len, shared).tiles + a.chunk_tiles - 1) / a.chunk_tiles : 0);
     }
@@ -542,10 +557,10 @@ __global__ __launch_bounds__(256) void attn_shared_join_kernel(const SharedArgs 
     }
 }
 
-template <int D, bool I8, bool TILED, bool WIDE>
+template <int D, bool I8, bool TILED, int WM>
 int attn_shared_start(const SharedArgs &a, hipStream_t stream) {
-    constexpr size_t bytes = std::max<size_t>(PrefixLds<D, prefix_tokens(WIDE)>::kBytes, sizeof(AttnWaveSums) + sizeof(AttnWaveOutputs<D>));
-    const auto kern = attn_shared_kernel<D, I8, TILED, WIDE>;
+    constexpr size_t bytes = std::max<size_t>(PrefixLds<D>::kBytes, sizeof(AttnWaveSums) + sizeof(AttnWaveOutputs<D>));
+    const auto kern = attn_shared_kernel<D, I8, TILED, WM>;
     if (bytes > 65536 && hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)bytes) != hipSuccess)
         return QK_ERR_LAUNCH;
@@ -566,10 +581,14 @@ int attn_shared_start(const SharedArgs &a, hipStream_t stream) {
     return st;
 }
 
+template <int D, bool I8, int WM>
+int attn_shared_tiled(const SharedArgs &a, bool tiled, hipStream_t stream) {
+    return tiled ? attn_shared_start<D, I8, true, WM>(a, stream) : attn_shared_start<D, I8, false, WM>(a, stream);
+}
+
 template <int D, bool I8>
 int attn_shared_dim(const SharedArgs &a, bool tiled, hipStream_t stream) {
-    int st = tiled ? (a.wide ? attn_shared_start<D, I8, true, true>(a, stream) : attn_shared_start<D, I8, true, false>(a, stream))
-                   : (a.wide ? attn_shared_start<D, I8, false, true>(a, stream) : attn_shared_start<D, I8, false, false>(a, stream));
+    int st = a.row_waves == 2 ? attn_shared_tiled<D, I8, 2>(a, tiled, stream) : attn_shared_tiled<D, I8, 4>(a, tiled, stream);
     const int64_t most = max_groups(256) / a.n_heads;  // sequences of one launch
     for (int64_t i = 0; i < a.n_seqs && st == QK_OK; i += most) {
         SharedArgs p = a;

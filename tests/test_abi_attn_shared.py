@@ -58,7 +58,7 @@ def _needed(heads, dim, seqs, q_heads, groups, max_shared, max_own):
     if groups and max_shared:
         g = min(groups, seqs)
         each = -(-seqs * per // g)
-        rows, tokens = (128, 64) if each > 32 else (32, 128)
+        rows, tokens = 128 if each > 64 else 64, 64
         tiles = -(-max_shared // tokens)
         chunk = max(1, min(tiles, -(-tiles * heads * g * -(-each // rows) // target)))
         n1 = -(-tiles // chunk)

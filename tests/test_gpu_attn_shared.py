@@ -171,7 +171,7 @@ class Batch:
 @pytest.mark.parametrize("dim", [32, 64, 96, 128, 160, 192, 224, 256])
 @pytest.mark.parametrize("size", [2, 20])
 def test_head_sizes(kind, dim, size):
-    """Few rows of a group (32 at a time) and many (128)."""
+    """Few rows of a group (64 at a time) and many (128)."""
     _say("dim", kind, dim, size)
     rng = np.random.default_rng(dim)
     Batch(kind, [(size, 150)], rng.integers(0, 70, size).tolist(), 2, 4, dim, 16, seed=1).check()
