@@ -105,11 +105,13 @@ __device__ __forceinline__ void attn_prefix_block(const SharedArgs &a, const int
             sh = a.shared[gi];
         }
         upto = tiles = (n + ROWS - 1) / ROWS;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int u = __shfl_up(upto, d);
-            if (lane >= d) upto += u;
-        }
+        // (sums of the lanes up to each: within rows of 16, then over the rows)
+        upto += __builtin_amdgcn_update_dpp(0, upto, 0x111, 0xF, 0xF, false);   // row_shr:1
+        upto += __builtin_amdgcn_update_dpp(0, upto, 0x112, 0xF, 0xF, false);
+        upto += __builtin_amdgcn_update_dpp(0, upto, 0x114, 0xF, 0xF, false);
+        upto += __builtin_amdgcn_update_dpp(0, upto, 0x118, 0xF, 0xF, false);
+        upto += __builtin_amdgcn_update_dpp(0, upto, 0x142, 0xA, 0xF, false);   // row_bcast:15
+        upto += __builtin_amdgcn_update_dpp(0, upto, 0x143, 0xC, 0xF, false);   // row_bcast:31
     };
     int total = 0;
     for (int g0 = 0; g0 < a.n_groups; g0 += 64) {
@@ -227,6 +229,14 @@ __device__ __forceinline__ void attn_prefix_block(const SharedArgs &a, const int
         }
     };
 
+    // q is asked for first, and then the places of the first rows
+    float qv[KS][8];
+    {
+        const float *q = a.q + seq * a.q_seq + head * a.q_head + 8 * g;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) __builtin_memcpy(qv[s], q + 16 * s, 32);
+    }
+    asm volatile("" ::: "memory");
     int id = 0;
     if (tid < BN) {
         const int p0 = table[page_of(token_of(0))], p1 = table[page_of(token_of(1))];
@@ -241,11 +251,7 @@ __device__ __forceinline__ void attn_prefix_block(const SharedArgs &a, const int
     h8_t qh[KS], ql[KS];
     int qexp;
     {
-        float qv[KS][8];
-        const float *q = a.q + seq * a.q_seq + head * a.q_head + 8 * g;
         float top = 0.0f;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) __builtin_memcpy(qv[s], q + 16 * s, 32);
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -263,14 +269,12 @@ __device__ __forceinline__ void attn_prefix_block(const SharedArgs &a, const int
             for (int i = 0; i < 8; ++i) qv[s][i] = ldexpf(qv[s][i], -qexp);
             split8(qv[s], qh[s], ql[s]);
             if constexpr (!I8) {
-                // (2^-14 for a low part of 0: 2^-27 of the row's largest)
-                u4_t h = __builtin_bit_cast(u4_t, qh[s]), l = __builtin_bit_cast(u4_t, ql[s]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if ((l[i] & 0x7FFFu) == 0 && (h[i] & 0x7FFFu) != 0) l[i] |= 0x0400u | (h[i] & 0x8000u);
-                    if ((l[i] & 0x7FFF0000u) == 0 && (h[i] & 0x7FFF0000u) != 0) l[i] |= 0x04000000u | (h[i] & 0x80000000u);
-                }
-                ql[s] = __builtin_bit_cast(h8_t, l);
+                // (2^-14 of the high part's sign is added where that is not 0: 2^-27 of the
+                // row's largest; the low part has the same sign or is 0)
+                typedef uint16_t s8_t __attribute__((ext_vector_type(8)));
+                const s8_t h = __builtin_bit_cast(s8_t, qh[s]);
+                const s8_t some = __builtin_elementwise_min((s8_t)(h & (uint16_t)0x7FFF), (s8_t)(uint16_t)1);
+                ql[s] += __builtin_bit_cast(h8_t, (s8_t)(some * (uint16_t)0x0400 | (h & (uint16_t)0x8000)));
             }
         }
         if constexpr (I8) qexp += 9;  // codes are held times 2^-9
@@ -470,10 +474,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_shared_kernel(cons
 
 // Joins the partial results of one (sequence, head): those of the shared
 // tokens' chunks, then those of its own.
-template <int D>
-__global__ __launch_bounds__(256) void attn_shared_join_kernel(const SharedArgs a) {
+template <int D, int T>
+__global__ __launch_bounds__(T) void attn_shared_join_kernel(const SharedArgs a) {
     constexpr int COLS = D / 4;
-    constexpr int ROWS = 256 / COLS;   // chunks at a time
+    constexpr int ROWS = T / COLS;     // chunks at a time
     constexpr int U = kAttnJoinUnroll;
     __shared__ __attribute__((aligned(16))) float so[ROWS][D];
     __shared__ float sl[ROWS], sm[ROWS];
@@ -536,7 +540,7 @@ __global__ __launch_bounds__(256) void attn_shared_join_kernel(const SharedArgs 
         }
     }
     __syncthreads();
-    for (int d = threadIdx.x; d < D; d += 256) {
+    for (int d = threadIdx.x; d < D; d += T) {
         float y = __builtin_nanf("");
         if (n > 0) {
             float m = sm[0];
@@ -589,11 +593,16 @@ int attn_shared_tiled(const SharedArgs &a, bool tiled, hipStream_t stream) {
 template <int D, bool I8>
 int attn_shared_dim(const SharedArgs &a, bool tiled, hipStream_t stream) {
     int st = a.row_waves == 2 ? attn_shared_tiled<D, I8, 2>(a, tiled, stream) : attn_shared_tiled<D, I8, 4>(a, tiled, stream);
+    // A wave joins a row of few partial results where there are many rows, four
+    // waves otherwise (8192 rows of 9 23 / 16 us with four / one, 2048 rows of 33 10 / 11).
+    const bool one_wave = a.slots <= 16 && (int64_t)a.n_seqs * a.n_heads >= 1024;
     const int64_t most = max_groups(256) / a.n_heads;  // sequences of one launch
     for (int64_t i = 0; i < a.n_seqs && st == QK_OK; i += most) {
         SharedArgs p = a;
         p.seq0 = (int)i;
-        st = launch(attn_shared_join_kernel<D>, dim3((unsigned)(std::min<int64_t>(a.n_seqs - i, most) * a.n_heads)), dim3(256), stream, p);
+        const dim3 grid((unsigned)(std::min<int64_t>(a.n_seqs - i, most) * a.n_heads));
+        st = one_wave ? launch(attn_shared_join_kernel<D, 64>, grid, dim3(64), stream, p)
+                      : launch(attn_shared_join_kernel<D, 256>, grid, dim3(256), stream, p);
     }
     return st;
 }
