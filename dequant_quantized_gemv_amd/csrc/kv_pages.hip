@@ -202,31 +202,165 @@ __global__ __launch_bounds__(kPlanThreads) void fork_plan_kernel(const ForkArgs 
     }
 }
 
+// Entry j of row i of the new table, `old` in the row that it is taken from (-1
+// past what is taken); the row's requests are those from `rank` up to `next`.
+__device__ __forceinline__ void fork_write(const ForkArgs &a, int i, int j, const Row &r, int old, int rank, int next, int found,
+                                           const int *list) {
+    // (a copied page is the one request that does not extend the row)
+    const int copied = next - rank > r.want - min(r.kept, r.want) ? r.had / a.page_size : -1;
+    const int request = j == copied ? rank : j >= r.kept && j < r.want ? rank + (copied >= 0) + j - r.kept : -1;
+    int p = old;
+    if (request >= 0) {
+        p = request < found ? list[request] : -1;
+        if (j == copied) {
+            a.src[i] = p >= 0 ? old : -1;
+            a.dst[i] = p;
+        }
+    }
+    a.out[i * a.ld_out + j] = p;
+    if (copied < 0 && j == 0) a.src[i] = a.dst[i] = -1;
+}
+
 __global__ __launch_bounds__(256) void fork_write_kernel(const ForkArgs a) {
     const int *list = reinterpret_cast<const int *>(a.ws + 2 * page_words(a.n_pages)), *first = list + a.n_pages;
     const int found = first[a.n_new + 1];
     for (int i = blockIdx.x; i < a.n_new; i += gridDim.x) {
         const Row r = fork_row(a, i);
-        const int rank = first[i];
-        // (a copied page is the one request that does not extend the row)
-        const int copied = first[i + 1] - rank > r.want - min(r.kept, r.want) ? r.had / a.page_size : -1;
         const int32_t *row = a.table + r.parent * a.ld_table;
-        for (int j = threadIdx.x; j < a.out_pages; j += 256) {
-            int p = -1;
-            if (j < r.kept) p = row[j];
-            const int request = j == copied ? rank : j >= r.kept && j < r.want ? rank + (copied >= 0) + j - r.kept : -1;
-            if (request >= 0) {
-                const int got = request < found ? list[request] : -1;
-                if (j == copied) {
-                    a.src[i] = got >= 0 ? p : -1;
-                    a.dst[i] = got;
-                }
-                p = got;
-            }
-            a.out[i * a.ld_out + j] = p;
-        }
-        if (copied < 0 && threadIdx.x == 0) a.src[i] = a.dst[i] = -1;
+        for (int j = threadIdx.x; j < a.out_pages; j += 256)
+            fork_write(a, i, j, r, j < r.kept ? row[j] : -1, first[i], first[i + 1], found, list);
+        if (a.out_pages == 0 && threadIdx.x == 0) a.src[i] = a.dst[i] = -1;
     }
+}
+
+// Tables and pools up to these sizes are planned by one workgroup, the bits in
+// LDS: one launch instead of four (4 rows of 63 pages 11.5 -> 5.x us, 64 of 256 19 -> x).
+constexpr int kOneRows = 1024, kOneList = 4096;
+constexpr int64_t kOnePages = 1 << 18, kOneEntries = 1 << 16;
+
+// Threads side by side in a row: 2^shift, 16 at least.
+__device__ __forceinline__ int row_shift(int pages) { return 32 - __clz((min(max(pages, 1), kPlanThreads) - 1) | 15); }
+
+// Marks the pages that rows hold: threads side by side in a row, several rows'
+// ids on their way at a time.  row(i) gives a row's ids and how many count.
+template <typename ROW>
+__device__ __forceinline__ void mark_rows(uint32_t *held, uint32_t *twice, int n_pages, int n, int pages, ROW row) {
+    constexpr int U = 8;
+    const int shift = row_shift(pages);
+    const int step = kPlanThreads >> shift;
+    for (int j0 = 0; j0 < pages; j0 += 1 << shift) {
+        const int j = j0 + (threadIdx.x & ((1 << shift) - 1));
+        for (int i0 = threadIdx.x >> shift; i0 < n; i0 += U * step) {
+            int p[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * step;
+                p[u] = -1;
+                if (i < n) {
+                    int kept;
+                    const int32_t *ids = row(i, kept);
+                    if (j < kept) p[u] = ids[j];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if ((unsigned)p[u] >= (unsigned)n_pages) continue;
+                const uint32_t bit = 1u << (p[u] & 31), was = atomicOr(&held[p[u] >> 5], bit);
+                if (twice != nullptr && (was & bit)) atomicOr(&twice[p[u] >> 5], bit);
+            }
+        }
+    }
+}
+
+// A new row: whose pages it takes over, how many, how many it has in all, and
+// which of them is to be copied (-1: none).
+struct __attribute__((aligned(16))) Taken { int parent, kept, want, copied; };
+
+__global__ __launch_bounds__(kPlanThreads) void fork_one_kernel(const ForkArgs a) {
+    extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
+    __shared__ Taken taken[kOneRows];
+    __shared__ int first[kOneRows], found_list[kOneList], sums[kPlanThreads / 64];
+    const int words = (int)page_words(a.n_pages);
+    uint32_t *held = lds, *twice = held + words;
+    for (int w = threadIdx.x; w < 2 * words; w += kPlanThreads) held[w] = 0;
+    Row mine{};
+    if ((int)threadIdx.x < a.n_new) {
+        mine = fork_row(a, threadIdx.x);
+        taken[threadIdx.x] = Taken{mine.parent, mine.kept, mine.want, -1};
+    }
+    __syncthreads();
+    mark_rows(held, twice, a.n_pages, a.n_new, min(a.in_pages, a.out_pages), [&](int i, int &kept) {
+        const Taken t = taken[i];
+        kept = t.kept;
+        return a.table + t.parent * a.ld_table;
+    });
+    __syncthreads();
+    // requests before each row
+    int need = 0, asked;
+    if ((int)threadIdx.x < a.n_new) {
+        need = mine.want - min(mine.kept, mine.want);
+        if (mine.has > mine.had && mine.had % a.page_size != 0) {
+            const int last = mine.had / a.page_size;
+            const int p = a.table[mine.parent * a.ld_table + last];
+            if ((unsigned)p < (unsigned)a.n_pages && (twice[p >> 5] >> (p & 31) & 1)) {
+                ++need;
+                taken[threadIdx.x].copied = last;
+            }
+        }
+    }
+    const int before = block_scan(need, asked, sums);
+    if ((int)threadIdx.x < a.n_new) first[threadIdx.x] = before;
+    // the free pages, each thread some words in a row
+    int *list = asked <= kOneList ? found_list : reinterpret_cast<int *>(a.ws);
+    const int each = (words + kPlanThreads - 1) / kPlanThreads, w0 = min((int)threadIdx.x * each, words), w1 = min(w0 + each, words);
+    auto free_in = [&](int w) { return ~held[w] & low_bits(min(32, a.n_pages - 32 * w)); };
+    int count = 0, found;
+    for (int w = w0; w < w1; ++w) count += __popc(free_in(w));
+    int rank = block_scan(count, found, sums);
+    for (int w = w0; w < w1 && rank < asked; ++w)
+        for (uint32_t free = free_in(w); free != 0 && rank < asked; free &= free - 1) list[rank++] = 32 * w + __builtin_ctz(free);
+    if (threadIdx.x == 0) *a.missing = max(0, asked - found);
+    __syncthreads();
+    // what rows take over, then what they asked for, a thread each
+    constexpr int U = 8;   // entries of a thread on the way at a time
+    const int shift = row_shift(a.out_pages), step = kPlanThreads >> shift;
+    for (int j0 = 0; j0 < a.out_pages; j0 += 1 << shift) {
+        const int j = j0 + (threadIdx.x & ((1 << shift) - 1));
+        for (int i0 = threadIdx.x >> shift; i0 < a.n_new; i0 += U * step) {
+            int p[U];
+            bool mine[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * step;
+                const Taken t = taken[min(i, a.n_new - 1)];
+                mine[u] = i < a.n_new && j < a.out_pages && j != t.copied && (j < t.kept || j >= t.want);
+                p[u] = mine[u] && j < t.kept ? a.table[t.parent * a.ld_table + j] : -1;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (mine[u]) a.out[(i0 + u * step) * a.ld_out + j] = p[u];
+        }
+    }
+    for (int q = threadIdx.x; q < asked; q += kPlanThreads) {
+        int lo = 0, hi = a.n_new - 1;   // the last row whose requests begin at or before q
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (first[mid] <= q) lo = mid;
+            else hi = mid - 1;
+        }
+        const Taken t = taken[lo];
+        const int at = q - first[lo], got = q < found ? list[q] : -1;
+        int j = t.kept + at;
+        if (t.copied >= 0) {
+            j = at == 0 ? t.copied : j - 1;
+            if (at == 0) {
+                a.src[lo] = got >= 0 ? a.table[t.parent * a.ld_table + j] : -1;
+                a.dst[lo] = got;
+            }
+        }
+        a.out[lo * a.ld_out + j] = got;
+    }
+    if ((int)threadIdx.x < a.n_new && taken[threadIdx.x].copied < 0) a.src[threadIdx.x] = a.dst[threadIdx.x] = -1;
 }
 
 __global__ __launch_bounds__(256) void compact_mark_kernel(const CompactArgs a) {
@@ -244,54 +378,95 @@ __device__ __forceinline__ int live_below(const uint32_t *held, const int *befor
     return before[p >> 5] + __popc(held[p >> 5] & low_bits(p & 31));
 }
 
-// The live pages before each word, then which pages move where: the m-th live
-// page from n on (n = the number of live pages) to the m-th free one below n.
-__global__ __launch_bounds__(kPlanThreads) void compact_plan_kernel(const CompactArgs a) {
-    __shared__ int sums[kPlanThreads / 64];
-    const int words = (int)page_words(a.n_pages);
-    const uint32_t *held = a.ws;
-    int *before = reinterpret_cast<int *>(a.ws + words);
-    int n = 0;
-    for (int w0 = 0; w0 < words; w0 += kPlanThreads) {
-        const int w = w0 + threadIdx.x;
-        int total;
-        const int b = block_scan(w < words ? __popc(held[w]) : 0, total, sums);
-        if (w < words) before[w] = n + b;
-        n += total;
+// The m-th free page (there is one): the last word with no more than m before it.
+__device__ __forceinline__ int free_page(const uint32_t *held, const int *before, int words, int m) {
+    int lo = 0, hi = words - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (32 * mid - before[mid] <= m) lo = mid;
+        else hi = mid - 1;
+    }
+    uint32_t free = ~held[lo];
+    for (int k = m - (32 * lo - before[lo]); k > 0; --k) free &= free - 1;
+    return 32 * lo + __builtin_ctz(free);
+}
+
+// The live pages before each word, their number, and how many of them stay.
+__device__ __forceinline__ void compact_plan(const CompactArgs &a, const uint32_t *held, int *before, int words, int (&sums)[kPlanThreads / 64]) {
+    const int each = (words + kPlanThreads - 1) / kPlanThreads, w0 = min((int)threadIdx.x * each, words), w1 = min(w0 + each, words);
+    int count = 0, n;
+    for (int w = w0; w < w1; ++w) count += __popc(held[w]);
+    int b = block_scan(count, n, sums);
+    for (int w = w0; w < w1; ++w) {
+        before[w] = b;
+        b += __popc(held[w]);
     }
     __syncthreads();
-    const int stay = n < a.n_pages ? live_below(held, before, n) : n;
-    for (int w = threadIdx.x; w < words; w += kPlanThreads) {
-        const uint32_t mask = low_bits(min(32, a.n_pages - 32 * w));
-        const uint32_t below = 32 * w >= n ? 0u : low_bits(n - 32 * w);   // pages below n
-        uint32_t moved = held[w] & ~below;
-        for (int m = max(before[w] - stay, 0); moved != 0; ++m, moved &= moved - 1) a.src[m] = 32 * w + __builtin_ctz(moved);
-        uint32_t hole = ~held[w] & below & mask;
-        for (int m = 32 * w - before[w]; hole != 0; ++m, hole &= hole - 1) a.dst[m] = 32 * w + __builtin_ctz(hole);
-    }
-    for (int m = n - stay + threadIdx.x; m < a.n_pages / 2; m += kPlanThreads) a.src[m] = a.dst[m] = -1;
     if (threadIdx.x == 0) {
         *a.live = n;
         before[words] = n;
-        before[words + 1] = stay;
+        before[words + 1] = n < a.n_pages ? live_below(held, before, n) : n;
     }
 }
 
+__global__ __launch_bounds__(kPlanThreads) void compact_plan_kernel(const CompactArgs a) {
+    __shared__ int sums[kPlanThreads / 64];
+    const int words = (int)page_words(a.n_pages);
+    compact_plan(a, a.ws, reinterpret_cast<int *>(a.ws + words), words, sums);
+}
+
+// Marking and plan of small tables and pools, the bits in LDS.
+__global__ __launch_bounds__(kPlanThreads) void compact_one_kernel(const CompactArgs a) {
+    extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
+    __shared__ int kept[kOneRows], sums[kPlanThreads / 64];
+    const int words = (int)page_words(a.n_pages);
+    for (int w = threadIdx.x; w < words; w += kPlanThreads) lds[w] = 0;
+    if ((int)threadIdx.x < a.n_rows) kept[threadIdx.x] = compact_kept(a, threadIdx.x);
+    __syncthreads();
+    mark_rows(lds, nullptr, a.n_pages, a.n_rows, a.max_pages, [&](int i, int &k) {
+        k = kept[i];
+        return a.table + i * a.ld_table;
+    });
+    __syncthreads();
+    compact_plan(a, lds, reinterpret_cast<int *>(a.ws + words), words, sums);
+    for (int w = threadIdx.x; w < words; w += kPlanThreads) a.ws[w] = lds[w];
+}
+
+// Which pages move where: the m-th live page from n on (n = the number of live
+// pages) to the m-th free one below n; and the rows with the new ids.
 __global__ __launch_bounds__(256) void compact_write_kernel(const CompactArgs a) {
     const int words = (int)page_words(a.n_pages);
+    const uint32_t *held = a.ws;
     const int *before = reinterpret_cast<const int *>(a.ws + words);
     const int n = before[words], stay = before[words + 1];
-    for (int i = blockIdx.x; i < a.n_rows; i += gridDim.x) {
-        const int kept = compact_kept(a, i);
-        for (int j = threadIdx.x; j < a.max_pages; j += 256) {
-            int p = -1;
-            if (j < kept) {
-                p = a.table[i * a.ld_table + j];
-                if (p >= n && p < a.n_pages) p = a.dst[live_below(a.ws, before, p) - stay];
-            }
-            a.out[i * a.ld_out + j] = p;
-        }
+    const int64_t all = (int64_t)gridDim.x * 256, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    // page p, live and moved or free and moved to
+    for (int64_t p = at; p < a.n_pages; p += all) {
+        const int live = live_below(held, before, (int)p);
+        const bool is = held[p >> 5] >> (p & 31) & 1;
+        if (is && p >= n) a.src[live - stay] = (int)p;
+        if (!is && p < n) a.dst[p - live] = (int)p;
     }
+    for (int64_t m = n - stay + at; m < a.n_pages / 2; m += all) a.src[m] = a.dst[m] = -1;
+    const int64_t entries = (int64_t)a.n_rows * a.max_pages;
+    for (int64_t e = at; e < entries; e += all) {
+        const uint32_t i = (uint32_t)e / (uint32_t)a.max_pages, j = (uint32_t)e - i * (uint32_t)a.max_pages;
+        int p = -1;
+        if ((int)j < compact_kept(a, (int)i)) {
+            p = a.table[i * a.ld_table + j];
+            if (p >= n && p < a.n_pages) p = free_page(held, before, words, live_below(held, before, p) - stay);
+        }
+        a.out[i * a.ld_out + j] = p;
+    }
+}
+
+// A launch with more LDS than a kernel has without asking.
+template <typename KERNEL, typename ARGS>
+int launch_big(KERNEL kern, dim3 grid, dim3 block, size_t lds, hipStream_t stream, const ARGS &a) {
+    if (lds > 16384 && hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)lds) != hipSuccess)
+        return QK_ERR_LAUNCH;
+    return launch_lds(kern, grid, block, lds, stream, a);
 }
 
 dim3 rows_grid(int64_t n) { return dim3((unsigned)std::min<int64_t>(std::max<int64_t>(n, 1), 16384)); }
@@ -315,6 +490,8 @@ int launch_kv_copy(const CopyArgs &a, hipStream_t stream) {
 }
 
 int launch_kv_fork(const ForkArgs &a, hipStream_t stream) {
+    if (a.n_new <= kOneRows && a.n_pages <= kOnePages && (int64_t)a.n_new * std::max(a.in_pages, a.out_pages) <= kOneEntries)
+        return launch_big(fork_one_kernel, dim3(1), dim3(kPlanThreads), 8 * (size_t)page_words(a.n_pages), stream, a);
     const int64_t words = 2 * page_words(a.n_pages);
     int st = launch(clear_kernel, rows_grid((words + 255) / 256), dim3(256), stream, a.ws, words);
     if (st == QK_OK) st = launch(fork_mark_kernel, rows_grid(a.n_new), dim3(256), stream, a);
@@ -325,10 +502,15 @@ int launch_kv_fork(const ForkArgs &a, hipStream_t stream) {
 
 int launch_kv_compact(const CompactArgs &a, hipStream_t stream) {
     const int64_t words = page_words(a.n_pages);
-    int st = launch(clear_kernel, rows_grid((words + 255) / 256), dim3(256), stream, a.ws, words);
-    if (st == QK_OK) st = launch(compact_mark_kernel, rows_grid(a.n_rows), dim3(256), stream, a);
-    if (st == QK_OK) st = launch(compact_plan_kernel, dim3(1), dim3(kPlanThreads), stream, a);
-    if (st == QK_OK) st = launch(compact_write_kernel, rows_grid(a.n_rows), dim3(256), stream, a);
+    int st;
+    if (a.n_rows <= kOneRows && a.n_pages <= kOnePages && (int64_t)a.n_rows * a.max_pages <= kOneEntries) {
+        st = launch_big(compact_one_kernel, dim3(1), dim3(kPlanThreads), 4 * (size_t)words, stream, a);
+    } else {
+        st = launch(clear_kernel, rows_grid((words + 255) / 256), dim3(256), stream, a.ws, words);
+        if (st == QK_OK) st = launch(compact_mark_kernel, rows_grid(a.n_rows), dim3(256), stream, a);
+        if (st == QK_OK) st = launch(compact_plan_kernel, dim3(1), dim3(kPlanThreads), stream, a);
+    }
+    if (st == QK_OK) st = launch(compact_write_kernel, rows_grid((std::max<int64_t>((int64_t)a.n_rows * a.max_pages, a.n_pages) + 255) / 256), dim3(256), stream, a);
     return st;
 }
 
