@@ -14,13 +14,17 @@ struct CopyPlane {
     int64_t page_stride, outer_stride, inner_stride;   // bytes
     uint32_t inner, run;                               // runs per outer step; bytes of a run (0: one run)
     int64_t bytes;                                     // of one page
+    int64_t pieces;                                    // of `piece` bytes in a page
+    int piece;
 };
 
 struct CopyArgs {
     CopyPlane plane[4];     // keys, values, and the scales of 8 bits
     int planes;
     const int32_t *src, *dst;
-    int64_t n;
+    int64_t first, n;       // pairs first .. n - 1
+    int64_t pieces;         // of a page's planes together
+    int chunks;             // workgroups of a pair, planes apart
     int n_pages;
 };
 

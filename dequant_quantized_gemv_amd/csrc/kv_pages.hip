@@ -25,20 +25,9 @@ typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
 // ---------------------------------------------------------------------------
 
 constexpr int kCopyThreads = 256;
-constexpr int kCopyUnroll = 4;    // pieces of a thread
+constexpr int kCopyUnroll = 2;    // pieces of a thread
 
-// Bytes of a piece: 16 where a plane's runs begin and end at multiples of 16.
-__host__ __device__ inline int piece_of(const CopyPlane &p) {
-    const uint64_t all = (uint64_t)(uintptr_t)p.base | (uint64_t)p.page_stride | (uint64_t)p.outer_stride |
-                         (uint64_t)p.inner_stride | (uint64_t)p.bytes | p.run;
-    return all % 16 == 0 ? 16 : 4;
-}
-__host__ __device__ inline int64_t copy_chunks(const CopyPlane &p) {
-    const int64_t chunk = (int64_t)piece_of(p) * kCopyThreads * kCopyUnroll;
-    return (p.bytes + chunk - 1) / chunk;
-}
-
-// A workgroup copies one chunk of one plane of one page.
+// Byte of piece `at` (bytes from the beginning) of a page.
 __device__ __forceinline__ int64_t run_offset(const CopyPlane &p, int64_t at) {
     if (p.run == 0) return at;
     if (p.bytes <= INT32_MAX) {
@@ -49,37 +38,79 @@ __device__ __forceinline__ int64_t run_offset(const CopyPlane &p, int64_t at) {
     return o * p.outer_stride + (r - o * p.inner) * p.inner_stride + at - r * p.run;
 }
 
-template <typename PIECE>
-__device__ __forceinline__ void copy_chunk(const CopyPlane &p, int from, int to, int64_t chunk) {
+constexpr int kCopyStep = kCopyThreads * kCopyUnroll;   // pieces of a workgroup
+
+// STREAM: with stores that leave the caches alone (2000 pages of 128 KB 57 -> 43 us,
+// 262 MB; no difference where the pages fit the caches).
+template <typename PIECE, bool STREAM>
+__device__ __forceinline__ void copy_chunk(const CopyPlane &p, int src, int dst, int64_t chunk) {
     PIECE x[kCopyUnroll];
     int64_t off[kCopyUnroll];
 #pragma unroll
     for (int u = 0; u < kCopyUnroll; ++u) {
-        const int64_t at = ((chunk * kCopyUnroll + u) * kCopyThreads + threadIdx.x) * (int64_t)sizeof(PIECE);
+        const int64_t at = (chunk * kCopyStep + u * kCopyThreads + threadIdx.x) * (int64_t)sizeof(PIECE);
         off[u] = at < p.bytes ? run_offset(p, at) : -1;
-        if (off[u] >= 0) x[u] = *reinterpret_cast<const PIECE *>(p.base + from * p.page_stride + off[u]);
+        if (off[u] >= 0) x[u] = *reinterpret_cast<const PIECE *>(p.base + src * p.page_stride + off[u]);
     }
 #pragma unroll
-    for (int u = 0; u < kCopyUnroll; ++u)
-        if (off[u] >= 0) *reinterpret_cast<PIECE *>(p.base + to * p.page_stride + off[u]) = x[u];
+    for (int u = 0; u < kCopyUnroll; ++u) {
+        PIECE *to = reinterpret_cast<PIECE *>(p.base + dst * p.page_stride + off[u]);
+        if (off[u] < 0) continue;
+        if (STREAM) __builtin_nontemporal_store(x[u], to);
+        else *to = x[u];
+    }
 }
 
-__global__ __launch_bounds__(kCopyThreads) void kv_copy_kernel(const CopyArgs a, const int chunks) {
-    const int64_t pair = blockIdx.x / (unsigned)chunks;
-    int64_t c = blockIdx.x - pair * chunks;
-    const int from = a.src[pair], to = a.dst[pair];
-    if ((unsigned)from >= (unsigned)a.n_pages || (unsigned)to >= (unsigned)a.n_pages || from == to) return;
+// Large pages: a workgroup takes one chunk of one plane of one pair.
+template <bool STREAM>
+__global__ __launch_bounds__(kCopyThreads) void kv_copy_kernel(const CopyArgs a) {
+    const int64_t pair = a.first + blockIdx.x / (unsigned)a.chunks;
+    int64_t c = blockIdx.x % (unsigned)a.chunks;
+    const int src = a.src[pair], dst = a.dst[pair];
+    if ((unsigned)src >= (unsigned)a.n_pages || (unsigned)dst >= (unsigned)a.n_pages || src == dst) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (i >= a.planes) return;
         const CopyPlane &p = a.plane[i];
-        const int64_t n = copy_chunks(p);
+        const int64_t n = (p.pieces + kCopyStep - 1) / kCopyStep;
         if (c < n) {
-            if (piece_of(p) == 16) copy_chunk<u4_t>(p, from, to, c);
-            else copy_chunk<uint32_t>(p, from, to, c);
+            if (p.piece == 16) copy_chunk<u4_t, STREAM>(p, src, dst, c);
+            else copy_chunk<uint32_t, STREAM>(p, src, dst, c);
             return;
         }
         c -= n;
+    }
+}
+
+// Small pages: the pieces of all planes of all pairs in a row, a thread some of
+// them (4000 pages of 2 KB 13 -> 4 us, in 8 bits 32 -> 5).
+__global__ __launch_bounds__(kCopyThreads) void kv_copy_small_kernel(const CopyArgs a) {
+    const uint32_t pieces = (uint32_t)a.pieces;
+    const int64_t begin = (int64_t)blockIdx.x * kCopyStep;
+    const int64_t pair0 = begin / pieces;
+    const uint32_t rest = (uint32_t)(begin - pair0 * pieces);
+#pragma unroll
+    for (int u = 0; u < kCopyUnroll; ++u) {
+        const uint32_t at = rest + u * kCopyThreads + threadIdx.x;
+        const uint32_t more = at / pieces;
+        int64_t piece = at - more * pieces;
+        const int64_t pair = a.first + pair0 + more;
+        if (pair >= a.n) return;
+        const int src = a.src[pair], dst = a.dst[pair];
+        if ((unsigned)src >= (unsigned)a.n_pages || (unsigned)dst >= (unsigned)a.n_pages || src == dst) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i >= a.planes || piece < 0) break;
+            const CopyPlane &p = a.plane[i];
+            if (piece < p.pieces) {
+                const int64_t off = run_offset(p, piece * p.piece);
+                const uint8_t *from = p.base + src * p.page_stride + off;
+                uint8_t *to = p.base + dst * p.page_stride + off;
+                if (p.piece == 16) *reinterpret_cast<u4_t *>(to) = *reinterpret_cast<const u4_t *>(from);
+                else *reinterpret_cast<uint32_t *>(to) = *reinterpret_cast<const uint32_t *>(from);
+            }
+            piece -= p.pieces;
+        }
     }
 }
 
@@ -473,17 +504,33 @@ dim3 rows_grid(int64_t n) { return dim3((unsigned)std::min<int64_t>(std::max<int
 
 }  // namespace
 
-int launch_kv_copy(const CopyArgs &a, hipStream_t stream) {
-    int64_t chunks = 0;
-    for (int i = 0; i < a.planes; ++i) chunks += copy_chunks(a.plane[i]);
-    if (chunks > max_groups(kCopyThreads)) return QK_ERR_INVALID_ARG;
-    const int64_t most = max_groups(kCopyThreads) / chunks;  // pairs of one launch
-    for (int64_t i = 0; i < a.n; i += most) {
-        CopyArgs p = a;
-        p.n = std::min(a.n - i, most);
-        p.src = a.src + i;
-        p.dst = a.dst + i;
-        const int st = launch(kv_copy_kernel, dim3((unsigned)(p.n * chunks)), dim3(kCopyThreads), stream, p, (int)chunks);
+int launch_kv_copy(const CopyArgs &args, hipStream_t stream) {
+    CopyArgs a = args;
+    int64_t bytes = 0, chunks = 0;
+    a.pieces = 0;
+    for (int i = 0; i < a.planes; ++i) {
+        CopyPlane &p = a.plane[i];
+        // 16 bytes where runs begin and end at multiples of them
+        const uint64_t all = (uint64_t)(uintptr_t)p.base | (uint64_t)p.page_stride | (uint64_t)p.outer_stride |
+                             (uint64_t)p.inner_stride | (uint64_t)p.bytes | p.run;
+        p.piece = all % 16 == 0 ? 16 : 4;
+        p.pieces = p.bytes / p.piece;
+        a.pieces += p.pieces;
+        chunks += (p.pieces + kCopyStep - 1) / kCopyStep;
+        bytes += p.bytes;
+    }
+    if (chunks > max_groups(kCopyThreads)) return QK_ERR_INVALID_ARG;   // (a page of 2^36 bytes)
+    a.chunks = (int)chunks;
+    const bool small = a.plane[0].pieces < kCopyStep / 2, stream_out = a.n * (double)bytes >= 64e6;
+    // pairs of one launch
+    const int64_t most = small ? max_groups(kCopyThreads) * kCopyStep / a.pieces - 1 : max_groups(kCopyThreads) / chunks;
+    for (int64_t i = 0; i < args.n; i += most) {
+        a.first = i;
+        a.n = std::min(args.n, i + most);
+        const dim3 grid((unsigned)(small ? ((a.n - i) * a.pieces + kCopyStep - 1) / kCopyStep : (a.n - i) * chunks)), block(kCopyThreads);
+        const int st = small        ? launch(kv_copy_small_kernel, grid, block, stream, a)
+                       : stream_out ? launch(kv_copy_kernel<true>, grid, block, stream, a)
+                                    : launch(kv_copy_kernel<false>, grid, block, stream, a);
         if (st != QK_OK) return st;
     }
     return QK_OK;

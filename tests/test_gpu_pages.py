@@ -265,6 +265,37 @@ def test_copy_leaves_what_lies_between():
     assert t.equal(whole.view(t.int16), before.view(t.int16))
 
 
+@pytest.mark.parametrize("kind", ["f16", "i8"])
+def test_many_large_and_many_small_pages(kind):
+    """More than the caches hold (other stores), and small pages of which a
+    workgroup takes several, pairs left out among them."""
+    t = torch()
+    for pairs, heads, page, dim in ((1200, 8, 16, 128), (3000, 1, 8, 32), (700, 2, 3, 32)):
+        n = 2 * pairs + 3
+        g = t.Generator(device="cuda")
+        g.manual_seed(pairs)
+        cache = qk.KVCache.empty(n, heads, page, dim, kind)
+        for x in (cache.k, cache.v):
+            x.random_(-127, 128, generator=g) if kind == "i8" else x.normal_(generator=g)
+        if kind == "i8":
+            cache.k_scale.normal_(generator=g)
+            cache.v_scale.normal_(generator=g)
+        ids = t.randperm(n, device="cuda", generator=g).to(t.int32)
+        src, dst = ids[:pairs].clone(), ids[pairs:2 * pairs].clone()
+        src[5], dst[9], src[17] = -1, n, dst[17]
+        ok = t.ones(pairs, dtype=t.bool, device="cuda")
+        ok[5] = ok[9] = False
+        want = []
+        for x in (cache.k, cache.v, cache.k_scale, cache.v_scale):
+            if x is not None:
+                w = x.clone()
+                w[dst[ok].long()] = x[src[ok].long()]
+                want.append((x, w))
+        qk.kv_copy(cache, src, dst)
+        for x, w in want:
+            assert t.equal(_bits(x), _bits(w)), (pairs, kind)
+
+
 def test_same_page_and_no_pairs():
     t = torch()
     cache = qk.KVCache.empty(4, 2, 16, 64)
