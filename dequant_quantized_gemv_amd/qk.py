@@ -850,17 +850,25 @@ def _ptr_bytes(t):
     return (t.data_ptr(), t.numel()) if t is not None else (None, 0)
 
 
+def _ids_check(torch, t, name, dim):
+    """_int32_check, quick where t is as it should be."""
+    if type(t) is not torch.Tensor or t.dtype is not torch.int32 or t.dim() != dim or not t.is_contiguous():
+        _int32_check(t, name, dim)
+
+
 def kv_copy(cache, src, dst, stream=None):
     """Copy whole pages of a paged cache (keys, values, scales): page dst[i] =
     page src[i], int32 (n,), as kv_fork and kv_compact list them.  A pair with
     an id outside the pool (-1) is left out.  No page may be written twice, nor
     written by one pair and read by another."""
-    _int32_check(src, "src", 1)
-    _int32_check(dst, "dst", 1)
-    if src.shape != dst.shape:
-        raise ValueError(f"src has {src.shape[0]} pages, dst {dst.shape[0]}")
+    import torch
+    _ids_check(torch, src, "src", 1)
+    _ids_check(torch, dst, "dst", 1)
+    n = src.shape[0]
+    if dst.shape[0] != n:
+        raise ValueError(f"src has {n} pages, dst {dst.shape[0]}")
     _on_device(cache.k, src, dst)
-    st = load().qk_kv_copy(cache.desc, src.data_ptr(), dst.data_ptr(), src.shape[0], _stream_of(cache.k, stream))
+    st = load().qk_kv_copy(cache.desc, src.data_ptr(), dst.data_ptr(), n, _stream_of(cache.k, stream))
     _check(st, "qk_kv_copy")
 
 
@@ -874,9 +882,9 @@ def kv_pages_workspace(n_rows, n_pages, device="cuda"):
     return torch.empty(need, dtype=torch.uint8, device=device)
 
 
-def _table_check(table, lens):
-    _int32_check(table, "table", 2)
-    _int32_check(lens, "lens", 1)
+def _table_check(torch, table, lens):
+    _ids_check(torch, table, "table", 2)
+    _ids_check(torch, lens, "lens", 1)
     if lens.shape[0] != table.shape[0]:
         raise ValueError(f"table has {table.shape[0]} rows, lens {lens.shape[0]}")
 
@@ -899,28 +907,28 @@ def kv_fork(table, lens, new_lens, page_size, n_pages, parent=None, out=None, wo
     import torch
     if stream is not None:
         return _on_stream(stream, table, kv_fork, table, lens, new_lens, page_size, n_pages, parent, out, workspace)
-    _table_check(table, lens)
-    _int32_check(new_lens, "new_lens", 1)
+    _table_check(torch, table, lens)
+    _ids_check(torch, new_lens, "new_lens", 1)
     _pages_check(page_size, n_pages)
+    rows, pages = table.shape
     n = new_lens.shape[0]
     if parent is not None:
-        _int32_check(parent, "parent", 1)
+        _ids_check(torch, parent, "parent", 1)
         if parent.shape[0] != n:
             raise ValueError(f"parent has {parent.shape[0]} rows, new_lens {n}")
     if out is None:
-        out = table.new_empty((n, table.shape[1]))
+        out, ld_out = table.new_empty((n, pages)), pages
     else:
-        _int32_check(out, "out", 2)
+        _ids_check(torch, out, "out", 2)
         if out.shape[0] != n:
             raise ValueError(f"out has {out.shape[0]} rows, new_lens {n}")
-    # (one allocation for the three small outputs)
-    small = table.new_empty(2 * n + 1)
-    src, dst, missing = small[:n], small[n:2 * n], small[2 * n:]
+        ld_out = out.stride(0)
+    src, dst, missing = table.new_empty(n), table.new_empty(n), table.new_empty(1)
     _on_device(table, lens, new_lens, parent, out, workspace)
     work, size = _ptr_bytes(_scratch(workspace, 0 if workspace is not None else qk_kv_pages_workspace(n, n_pages), table.device))
-    st = load().qk_kv_fork(table.data_ptr(), table.stride(0), lens.data_ptr(), table.shape[0], table.shape[1],
+    st = load().qk_kv_fork(table.data_ptr(), table.stride(0), lens.data_ptr(), rows, pages,
                            parent.data_ptr() if parent is not None else None, new_lens.data_ptr(), n, out.shape[1],
-                           page_size, n_pages, out.data_ptr(), out.stride(0), src.data_ptr(), dst.data_ptr(),
+                           page_size, n_pages, out.data_ptr(), ld_out, src.data_ptr(), dst.data_ptr(),
                            missing.data_ptr(), work, size, _stream_of(table))
     _check(st, "qk_kv_fork")
     return out, src, dst, missing
@@ -935,12 +943,13 @@ def kv_compact(table, lens, page_size, n_pages, out=None, workspace=None, stream
     import torch
     if stream is not None:
         return _on_stream(stream, table, kv_compact, table, lens, page_size, n_pages, out, workspace)
-    _table_check(table, lens)
+    _table_check(torch, table, lens)
     _pages_check(page_size, n_pages)
+    rows, pages = table.shape
     if out is None:
-        out = table.new_empty(table.shape)
+        out = table.new_empty((rows, pages))
     else:
-        _int32_check(out, "out", 2)
+        _ids_check(torch, out, "out", 2)
         if out.shape != table.shape:
             raise ValueError(f"out must be {tuple(table.shape)}, got {tuple(out.shape)}")
     n = n_pages // 2
@@ -948,7 +957,7 @@ def kv_compact(table, lens, page_size, n_pages, out=None, workspace=None, stream
     _on_device(table, lens, out, workspace)
     work, size = _ptr_bytes(_scratch(workspace, 0 if workspace is not None else qk_kv_pages_workspace(table.shape[0], n_pages),
                                      table.device))
-    st = load().qk_kv_compact(table.data_ptr(), table.stride(0), lens.data_ptr(), table.shape[0], table.shape[1],
+    st = load().qk_kv_compact(table.data_ptr(), table.stride(0), lens.data_ptr(), rows, pages,
                               page_size, n_pages, out.data_ptr(), out.stride(0), src.data_ptr(), dst.data_ptr(),
                               live.data_ptr(), work, size, _stream_of(table))
     _check(st, "qk_kv_compact")
@@ -980,11 +989,12 @@ def attn_decode_shared(cache, q, table, lens, starts, shared, scale=None, max_le
     if out_dtype not in ("f32", "f16"):
         raise ValueError(f"out_dtype must be 'f32' or 'f16', got {out_dtype!r}")
     code, dt = (QK_F32, torch.float32) if out_dtype == "f32" else (QK_F16, torch.float16)
-    _table_check(table, lens)
-    _int32_check(starts, "starts", 1)
-    _int32_check(shared, "shared", 1)
-    if starts.shape[0] != shared.shape[0] + 1:
-        raise ValueError(f"starts has {starts.shape[0]} entries for {shared.shape[0]} groups (one more than groups)")
+    _table_check(torch, table, lens)
+    _ids_check(torch, starts, "starts", 1)
+    _ids_check(torch, shared, "shared", 1)
+    groups = shared.shape[0]
+    if starts.shape[0] != groups + 1:
+        raise ValueError(f"starts has {starts.shape[0]} entries for {groups} groups (one more than groups)")
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise TypeError("q must be a float32 tensor (n_seqs, n_q_heads, head_dim)")
     n, heads, dim = q.shape[0], q.shape[1], cache.head_dim
@@ -1011,7 +1021,7 @@ def attn_decode_shared(cache, q, table, lens, starts, shared, scale=None, max_le
     q_head, y_head = (q.stride(1), y.stride(1)) if heads > 1 else (0, 0)
     st = load().qk_attn_decode_shared(cache.desc, q.data_ptr(), _row_stride(q), q_head, n, heads, table.data_ptr(),
                                       table.stride(0), lens.data_ptr(), max_len, starts.data_ptr(), shared.data_ptr(),
-                                      shared.shape[0], max_shared, max_own, dim ** -0.5 if scale is None else scale, code,
+                                      groups, max_shared, max_own, dim ** -0.5 if scale is None else scale, code,
                                       y.data_ptr(), _row_stride(y), y_head, work, size, _stream_of(q))
     _check(st, "qk_attn_decode_shared")
     return y
@@ -1046,14 +1056,26 @@ def token_logprobs(logits, ids=None, top=0, scale=1.0, workspace=None, stream=No
         raise ValueError(f"scale must be positive and finite, got {scale}")
     lp, ip, ld_ids, m = None, None, 0, 0
     if ids is not None:
-        _int32_check(ids, "ids", ids.dim() if isinstance(ids, torch.Tensor) and ids.dim() in (1, 2) else 2)
+        _ids_check(torch, ids, "ids", ids.dim() if isinstance(ids, torch.Tensor) and ids.dim() in (1, 2) else 2)
         if ids.shape[0] != n:
             raise ValueError(f"ids has {ids.shape[0]} rows, logits {n}")
         m = ids.shape[1] if ids.dim() == 2 else 1
-        lp, ip, ld_ids = logits.new_empty(ids.shape, dtype=torch.float32), ids.data_ptr(), ids.stride(0)
-    entropy = logits.new_empty(n, dtype=torch.float32)
-    best_ids = logits.new_empty((n, top), dtype=torch.int32) if top else None
-    best = logits.new_empty((n, top), dtype=torch.float32) if top else None
+        ip, ld_ids = ids.data_ptr(), ids.stride(0)
+    best_ids = best = None
+    if dtype is torch.float32:   # (without a type of its own an allocation is quicker)
+        entropy = logits.new_empty(n)
+        if ids is not None:
+            lp = logits.new_empty(ids.shape)
+        if top:
+            best = logits.new_empty((n, top))
+    else:
+        entropy = logits.new_empty(n, dtype=torch.float32)
+        if ids is not None:
+            lp = entropy.new_empty(ids.shape)
+        if top:
+            best = entropy.new_empty((n, top))
+    if top:
+        best_ids = logits.new_empty((n, top), dtype=torch.int32)
     _on_device(logits, ids, workspace)
     work, size = _ptr_bytes(_scratch(workspace, 0 if workspace is not None else qk_token_logprobs_workspace(n, vocab, top),
                                      logits.device))
