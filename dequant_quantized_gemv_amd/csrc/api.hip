@@ -258,7 +258,14 @@ bool attn_fill(const qk_kv_cache &c, qk::AttnArgs &a, const float *q, int64_t q_
 }
 
 // Sizes and splits of an attention with shared first tokens: tiles of 64 query
-// rows where the groups have no more than that on average, else of 128.
+// rows where the groups have no more than that on average or the chunks of shared
+// tokens would be short, else of 128 (32 query heads over 8 of 128, 64 sequences:
+// 2048 shared tokens 33 / 36 us with 64 / 128 rows, 8192 47 / 48, 16384 68 / 65,
+// 32768 114 / 102; 128 sequences: 2048 43 / 51, 16384 105 / 103; 2 heads of 256, 64
+// sequences of 16384 85 / 77).
+// Chunks of less than four tiles only where there are few tiles at all (8 sequences:
+// 1024 tokens 13 us in chunks of one, 15.5 of four, 4096 tokens 21 of two, 17.5 of four).
+constexpr int64_t kPrefixLong = 12, kPrefixShort = 4;   // tiles
 int shared_plan(const qk_kv_cache &c, int64_t n_seqs, int64_t n_q_heads, int64_t n_groups, int64_t max_len,
                 int64_t max_shared, int64_t max_own, qk::SharedArgs &a) {
     if (n_groups < 0 || n_groups > kMaxDim || max_shared < 0 || max_own < 1 || max_len < 1 || max_len > (int64_t(1) << 30) ||
@@ -277,13 +284,17 @@ int shared_plan(const qk_kv_cache &c, int64_t n_seqs, int64_t n_q_heads, int64_t
     if (n_groups > 0 && max_shared > 0) {
         const int64_t groups = std::min(n_groups, n_seqs);
         const int64_t each = (n_seqs * a.group + groups - 1) / groups;   // query rows of a group
-        a.row_waves = each > 64 ? 4 : 2;
-        const int64_t rows = qk::prefix_rows(a.row_waves), tokens = qk::kPrefixTokens;
-        // row tiles at most, and about as many as there will be
-        a.row_tiles = (int)(n_seqs * a.group / rows + groups);
-        const int64_t about = groups * ((each + rows - 1) / rows);
-        const int64_t tiles = (max_shared + tokens - 1) / tokens, target = attn_target(c);
-        a.prefix_tiles = (int)std::max<int64_t>(1, std::min(tiles, (tiles * a.n_kv * about + target - 1) / target));
+        const int64_t tokens = qk::prefix_tokens((int)c.head_dim), tiles = (max_shared + tokens - 1) / tokens, target = attn_target(c);
+        // 128 rows at a time only where that leaves long chunks
+        for (a.row_waves = each > 64 ? 4 : 2;; a.row_waves = 2) {
+            const int64_t rows = qk::prefix_rows(a.row_waves);
+            // row tiles at most, and about as many as there will be
+            a.row_tiles = (int)(n_seqs * a.group / rows + groups);
+            const int64_t about = groups * ((each + rows - 1) / rows);
+            a.prefix_tiles = (int)std::max<int64_t>(tiles >= 8 * kPrefixShort ? kPrefixShort : 1,
+                                                    std::min(tiles, (tiles * a.n_kv * about + target - 1) / target));
+            if (a.row_waves == 2 || a.prefix_tiles * (c.head_dim <= 128 ? 1 : 2) >= kPrefixLong) break;
+        }
         a.prefix_chunks = (int)((tiles + a.prefix_tiles - 1) / a.prefix_tiles);
     }
     if ((int64_t)a.n_kv * a.prefix_chunks > (1 << 22)) return QK_ERR_INVALID_ARG;
@@ -302,7 +313,7 @@ size_t shared_workspace(const qk_kv_cache &c, const qk::SharedArgs &a) {
 size_t shared_workspace_bound(const qk_kv_cache &c, const qk::SharedArgs &a) {
     const int64_t target = attn_target(c), seqs = a.n_seqs, heads = a.n_heads;
     int64_t parts = 0;
-    if (a.max_shared > 0) parts = std::min(seqs * heads * ((a.max_shared + qk::kPrefixTokens - 1) / qk::kPrefixTokens), seqs * heads + target * qk::prefix_rows(4));
+    if (a.max_shared > 0) parts = std::min(seqs * heads * ((a.max_shared + 63) / 64), seqs * heads + target * qk::prefix_rows(4));
     const int64_t tiles = ((int64_t)a.max_own + 2 * qk::kAttnTile - 2) / qk::kAttnTile, row = (int64_t)a.n_kv * a.head_tiles;
     parts += heads * std::min(seqs * ((tiles + qk::kAttnWaves - 1) / qk::kAttnWaves), target / row + seqs);
     return 4 * (size_t)parts * (size_t)qk::attn_part_floats((int)c.head_dim);

@@ -74,9 +74,10 @@ __host__ __device__ inline AttnSpan own_span(int len, int shared) {
     return AttnSpan{len, shared, start, 0, (len - start + kAttnTile - 1) / kAttnTile};
 }
 
-// Tokens of a tile of the shared ones, and query rows of one: `row_waves` (2 or
-// 4) of a workgroup's waves have rows of their own.
-constexpr int kPrefixTokens = 64;
+// Tokens of a tile of the shared ones (as many bytes on their way with small
+// heads), and query rows of one: `row_waves` (2 or 4) of a workgroup's waves have
+// rows of their own.
+constexpr int prefix_tokens(int head_dim) { return head_dim <= 64 ? 128 : 64; }
 constexpr int prefix_rows(int row_waves) { return 32 * row_waves; }
 
 struct StoreArgs {

@@ -40,7 +40,7 @@ typedef float f16_t __attribute__((ext_vector_type(16)));
 
 template <int D>
 struct PrefixLds {
-    static constexpr int BN = kPrefixTokens;
+    static constexpr int BN = prefix_tokens(D);
     static constexpr int kRow = 2 * D + 16;    // bytes of a key row (the 16 keep 16-byte reads of 16 rows off each other's banks)
     static constexpr int kDim = 2 * BN + 16;   // bytes of a dimension's values
     static constexpr int kValues = BN * kRow;
@@ -73,7 +73,7 @@ __device__ __forceinline__ void split8_mixed(const float (&p)[8], float minus, h
 
 template <int D, bool I8, int WM>
 __device__ __forceinline__ void attn_prefix_block(const SharedArgs &a, const int block, uint8_t *lds) {
-    constexpr int ROWS = prefix_rows(WM), BN = kPrefixTokens;
+    constexpr int ROWS = prefix_rows(WM), BN = prefix_tokens(D);
     constexpr int WN = 4 / WM;                 // waves that take different tokens of the same rows
     constexpr int SUBS = BN / WN / 32;         // 32-token blocks of a wave
     constexpr int ES = I8 ? 1 : 2;
@@ -496,7 +496,7 @@ __global__ __launch_bounds__(T) void attn_shared_join_kernel(const SharedArgs a)
     const int row = threadIdx.x / COLS, col = threadIdx.x % COLS;
     int n1 = 0, n = 0;
     if (fine) {
-        const int64_t chunk = (int64_t)a.prefix_tiles * kPrefixTokens;
+        const int64_t chunk = (int64_t)a.prefix_tiles * prefix_tokens(D);
         n1 = shared > 0 ? (int)((shared + chunk - 1) / chunk) : 0;
         n = n1 + (len > shared ? (own_span(len, shared).tiles + a.chunk_tiles - 1) / a.chunk_tiles : 0);
     }

@@ -58,9 +58,11 @@ def _needed(heads, dim, seqs, q_heads, groups, max_shared, max_own):
     if groups and max_shared:
         g = min(groups, seqs)
         each = -(-seqs * per // g)
-        rows, tokens = 128 if each > 64 else 64, 64
-        tiles = -(-max_shared // tokens)
-        chunk = max(1, min(tiles, -(-tiles * heads * g * -(-each // rows) // target)))
+        tiles = -(-max_shared // (128 if dim <= 64 else 64))
+        for rows in ((128, 64) if each > 64 else (64,)):
+            chunk = max(4 if tiles >= 32 else 1, min(tiles, -(-tiles * heads * g * -(-each // rows) // target)))
+            if chunk * (1 if dim <= 128 else 2) >= 12:
+                break
         n1 = -(-tiles // chunk)
     tiles = -(-(max_own + 31) // 32)
     rows = seqs * heads * -(-per // 16)
