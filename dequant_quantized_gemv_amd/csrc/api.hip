@@ -279,6 +279,11 @@ int shared_plan(const qk_kv_cache &c, int64_t n_seqs, int64_t n_q_heads, int64_t
     a.max_shared = (int)max_shared;
     a.max_own = (int)max_own;
     if (n_seqs == 0) return QK_OK;
+    // A wave takes a chunk of own tokens alone where there are many and they are
+    // short: 2048 of up to 200 tokens 63 / 60 us with four waves / one, of 256 84 / 81,
+    // of 1000 100 / 111; 512 of 256 27 / 31.
+    const bool alone = max_own <= 480 && n_seqs * a.n_kv * a.head_tiles >= 4 * (int64_t)qk::device_cus();
+    a.own_waves = alone ? 1 : qk::kAttnWaves;
     a.prefix_chunks = 0;
     a.prefix_tiles = 1;
     if (n_groups > 0 && max_shared > 0) {
@@ -286,14 +291,15 @@ int shared_plan(const qk_kv_cache &c, int64_t n_seqs, int64_t n_q_heads, int64_t
         const int64_t each = (n_seqs * a.group + groups - 1) / groups;   // query rows of a group
         const int64_t tokens = qk::prefix_tokens((int)c.head_dim), tiles = (max_shared + tokens - 1) / tokens, target = attn_target(c);
         // 128 rows at a time only where that leaves long chunks
-        for (a.row_waves = each > 64 ? 4 : 2;; a.row_waves = 2) {
+        // (and with large heads, whose tiles are of 64 tokens, 64 at least)
+        for (a.row_waves = each > 64 ? 4 : each > 32 || tokens < 128 ? 2 : 1;; a.row_waves = 2) {
             const int64_t rows = qk::prefix_rows(a.row_waves);
             // row tiles at most, and about as many as there will be
             a.row_tiles = (int)(n_seqs * a.group / rows + groups);
             const int64_t about = groups * ((each + rows - 1) / rows);
             a.prefix_tiles = (int)std::max<int64_t>(tiles >= 8 * kPrefixShort ? kPrefixShort : 1,
                                                     std::min(tiles, (tiles * a.n_kv * about + target - 1) / target));
-            if (a.row_waves == 2 || a.prefix_tiles * (c.head_dim <= 128 ? 1 : 2) >= kPrefixLong) break;
+            if (a.row_waves <= 2 || a.prefix_tiles * (c.head_dim <= 128 ? 1 : 2) >= kPrefixLong) break;
         }
         a.prefix_chunks = (int)((tiles + a.prefix_tiles - 1) / a.prefix_tiles);
     }

@@ -42,7 +42,8 @@ struct SharedArgs : AttnArgs {
     int prefix_tiles, prefix_chunks, slots;   // tiles of a chunk of shared tokens; chunks
     int row_tiles, row_waves;                 // tiles of query rows, at most; waves with rows of their own in each
     int seq0, group0;                         // first sequence, first eight of workgroups of this launch
-    int own_blocks;                           // workgroups of sequences' own tokens in it
+    int own_blocks, own_items;                // workgroups of sequences' own tokens in it, chunks of those
+    int own_waves;                            // waves of such a chunk, 4 or 1
 };
 
 // One partial result: the running maximum and sum, then head_dim outputs.
@@ -75,8 +76,8 @@ __host__ __device__ inline AttnSpan own_span(int len, int shared) {
 }
 
 // Tokens of a tile of the shared ones (as many bytes on their way with small
-// heads), and query rows of one: `row_waves` (2 or 4) of a workgroup's waves have
-// rows of their own.
+// heads), and query rows of one: `row_waves` (4, 2, or with tiles of 128 tokens 1)
+// of a workgroup's waves have rows of their own.
 constexpr int prefix_tokens(int head_dim) { return head_dim <= 64 ? 128 : 64; }
 constexpr int prefix_rows(int row_waves) { return 32 * row_waves; }
 

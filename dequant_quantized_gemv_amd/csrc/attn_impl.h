@@ -163,7 +163,8 @@ __device__ __forceinline__ int shared_tokens(const SharedArgs &a, int seq, int l
 typedef float AttnWaveSums[kAttnWaves][kAttnHeads][2];
 template <int D> using AttnWaveOutputs = float[kAttnWaves][kAttnHeads][D + 4];
 
-// Workgroup `block` of `blocks`.
+// Workgroup `block` of `blocks`, or, where the wave takes a sequence's own tokens
+// alone, four of `blocks`.
 template <int D, bool I8, bool TILED, class ARGS>
 __device__ __forceinline__ void attn_decode_block(const ARGS &a, const int block, const int blocks, AttnWaveSums &sm, AttnWaveOutputs<D> &so) {
     constexpr bool SHARED = std::is_same_v<ARGS, SharedArgs>;
@@ -175,12 +176,20 @@ __device__ __forceinline__ void attn_decode_block(const ARGS &a, const int block
     typedef const __attribute__((address_space(4))) int32_t cint_t;  // scalar loads
 
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, j = lane & 15;
     // Chunks outermost: workgroups go round the XCDs in turn, so with chunks
     // innermost the chunks that only long sequences have would meet on the
     // same XCDs; and a sequence's first chunks, which are whole, start first.
-    int b = block;
+    int b = block, waves = kAttnWaves;   // of a chunk
+    if constexpr (SHARED) {
+        if (a.own_waves == 1) {
+            waves = 1;
+            b = b * kAttnWaves + wave;
+            wave = 0;
+            if (b >= blocks) return;
+        }
+    }
     const int rows = blocks / a.nchunks;
     const int chunk = b / rows;
     b -= chunk * rows;
@@ -516,17 +525,17 @@ __device__ __forceinline__ void attn_decode_block(const ARGS &a, const int block
         }
         load_k(at);
         load_v(at);
-        at = locate(min(v + kAttnWaves, tend - 1));
+        at = locate(min(v + waves, tend - 1));
         asm volatile("" ::: "memory");
         split_q();
-        for (; v + kAttnWaves < tend; v += kAttnWaves) {
-            const int n = v + kAttnWaves;
+        for (; v + waves < tend; v += waves) {
+            const int n = v + waves;
             scores();
             load_k(at);
             probabilities(v);
             outputs();
             load_v(at);
-            at = locate(min(n + kAttnWaves, tend - 1));
+            at = locate(min(n + waves, tend - 1));
         }
         scores();
         probabilities(v);
@@ -534,6 +543,25 @@ __device__ __forceinline__ void attn_decode_block(const ARGS &a, const int block
     }
     l = quad_rows_sum(l);
     if (__any(bad)) l = __builtin_nanf("");
+
+    if constexpr (SHARED) {
+        if (waves == 1) {
+            if (j >= nh) return;
+            float *part = a.part + ((int64_t)(seq * (int64_t)a.n_heads + head0 + j) * a.slots + a.prefix_chunks + chunk) * attn_part_floats(D);
+            if (g == 0) {
+                part[0] = m;
+                part[1] = l;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < DPL; c += 2) {
+                    const float two[2] = {o[c][i], o[c + 1][i]};
+                    __builtin_memcpy(part + 4 + (4 * g + i) * DPL + c, two, 8);
+                }
+            return;
+        }
+    }
 
     // join the waves
     if (g == 0) {

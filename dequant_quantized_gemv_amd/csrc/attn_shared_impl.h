@@ -18,10 +18,11 @@
 // the same, the values' tokens are stored in the order that the results have.
 // The next tile's rows are in registers while one is worked on.
 // A workgroup has 128 rows, every wave all tokens of a tile, or, where groups
-// have no more, 64, the waves in two halves with half of the tokens each, joined in
-// LDS at the end: half as many partial results per row (8 rows of 32768 tokens
-// 44.3 / 45.8 us with 64 / 128, 64 rows 114 / 102; 32 rows and a tile of 128 tokens
-// lost to both: 59).
+// have no more, 64 or 32, two or four waves taking parts of a tile's tokens for the
+// same rows, joined in LDS at the end: fewer partial results per row, and no
+// waves without rows (8 rows of 32768 tokens of head size 128 44.3 / 45.8 us with
+// 64 / 128, 64 rows 114 / 102; 32 rows take tiles of 128 tokens, which registers hold up
+// to head size 64: 32 groups of 16 rows there 28.2 -> 25.5, at 128 spilled, 44 -> 59).
 //
 // Scores as in the decode kernel: exact keys, q in two fp16 parts.  The low
 // part is never 0 beside a high part that is not, so that a key which
@@ -464,7 +465,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_shared_kernel(cons
     if ((int)blockIdx.x < a.own_blocks) {
         auto &sm = *reinterpret_cast<AttnWaveSums *>(lds);
         auto &so = *reinterpret_cast<AttnWaveOutputs<D> *>(lds + sizeof(AttnWaveSums));
-        attn_decode_block<D, I8, TILED>(a, blockIdx.x, a.own_blocks, sm, so);
+        attn_decode_block<D, I8, TILED>(a, blockIdx.x, a.own_items, sm, so);
     } else {
         // (a multiple of 8 behind the own tokens' workgroups, for the XCDs)
         const int block = (int)blockIdx.x - (a.own_blocks + 7) / 8 * 8;
@@ -571,12 +572,14 @@ int attn_shared_start(const SharedArgs &a, hipStream_t stream) {
     // workgroups of the shared tokens in eights, one for each XCD, and of a sequence's own
     const int64_t eights = a.prefix_chunks > 0 ? ((int64_t)a.n_kv * a.prefix_chunks + 7) / 8 * a.row_tiles : 0;
     const int64_t each = (int64_t)a.n_kv * a.head_tiles * a.nchunks, most = max_groups(256) / 8 * 8;
+    const int64_t items = kAttnWaves / a.own_waves;   // of a workgroup
     auto go = [&](int64_t seq, int64_t n, int64_t eight, int64_t ne) {
         SharedArgs p = a;
         p.seq0 = (int)seq;
-        p.own_blocks = (int)(n * each);
+        p.own_items = (int)(n * each);
+        p.own_blocks = (int)((n * each + items - 1) / items);
         p.group0 = (int)eight;
-        return launch_lds(kern, dim3((unsigned)((n * each + 7) / 8 * 8 + 8 * ne)), dim3(256), bytes, stream, p);
+        return launch_lds(kern, dim3((unsigned)((p.own_blocks + 7) / 8 * 8 + 8 * ne)), dim3(256), bytes, stream, p);
     };
     if (a.n_seqs * each <= most - 8 * eights) return go(0, a.n_seqs, 0, eights);
     int st = QK_OK;
@@ -592,7 +595,11 @@ int attn_shared_tiled(const SharedArgs &a, bool tiled, hipStream_t stream) {
 
 template <int D, bool I8>
 int attn_shared_dim(const SharedArgs &a, bool tiled, hipStream_t stream) {
-    int st = a.row_waves == 2 ? attn_shared_tiled<D, I8, 2>(a, tiled, stream) : attn_shared_tiled<D, I8, 4>(a, tiled, stream);
+    int st;
+    if (a.row_waves == 4) st = attn_shared_tiled<D, I8, 4>(a, tiled, stream);
+    else if (a.row_waves == 2) st = attn_shared_tiled<D, I8, 2>(a, tiled, stream);
+    else if constexpr (prefix_tokens(D) == 128) st = attn_shared_tiled<D, I8, 1>(a, tiled, stream);
+    else return QK_ERR_INVALID_ARG;
     // A wave joins a row of few partial results where there are many rows, four
     // waves otherwise (8192 rows of 9 23 / 16 us with four / one, 2048 rows of 33 10 / 11).
     const bool one_wave = a.slots <= 16 && (int64_t)a.n_seqs * a.n_heads >= 1024;

@@ -236,6 +236,32 @@ def test_long(kind, heads, group, dim, size, shared, own):
 
 
 @pytest.mark.parametrize("kind", ["f16", "i8"])
+@pytest.mark.parametrize("heads,group,dim,page,n,layout", [
+    (8, 1, 64, 24, 131, "phs"), (8, 4, 128, 16, 130, "phs"), (4, 17, 32, 16, 129, "psh"), (1, 2, 64, 7, 1025, "phs"),
+    (1, 1, 96, 32, 1027, "phs"), (16, 1, 256, 16, 66, "phs")])
+def test_many_sequences(kind, heads, group, dim, page, n, layout):
+    """A wave takes a sequence's own tokens alone (not where they may be many)."""
+    _say("many", kind, heads, group, dim, page, n, layout)
+    rng = np.random.default_rng(n)
+    own = [None if rng.random() < 0.05 else int(rng.choice([0, 1, 7, 32, 33, 65, 100])) for _ in range(n)]
+    own[5], own[n - 1] = 480, 300
+    groups = [(20, 150), (3, 40), (1, 129), (32, 65)]
+    for s in range(2, 2 + sum(g[0] for g in groups)):
+        own[s] = own[s] if own[s] != 0 or s % 2 else 1
+    b = Batch(kind, groups, own, heads, group, dim, page, seed=11, lead=2, layout=layout)
+    b.check()
+    b.check(bounds=(b.max_len, b.max_shared, b.max_len))
+    # a page outside the pool: its sequence alone is NaN
+    y = b.run()
+    at = b.lens[5] // b.page - 1
+    b.dtable[5, at] = b.n_pages
+    got = b.run()
+    assert np.isnan(got[5]).all()
+    got[5] = y[5]
+    assert np.array_equal(got, y)
+
+
+@pytest.mark.parametrize("kind", ["f16", "i8"])
 def test_half_outputs_scales_and_bounds(kind):
     b = Batch(kind, [(5, 260), (20, 90)], [9] * 25, 2, 4, 64, 16, seed=7)
     b.check(out="f16")
