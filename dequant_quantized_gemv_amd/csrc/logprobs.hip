@@ -11,6 +11,12 @@
 //
 // The best are chosen by (logit, lowest index) as one 64-bit number, so that
 // they do not hang on the order in which anything arrives.
+//
+// Many rows are bound by reading the logits once: 2048 of 32000 in fp32 51 us without
+// the best (262 MB, 5.1 TB/s), 54 with 5 of them, 66 with 64.  In fp16 46, which is
+// half the bytes and the same instructions: one workgroup of 1024 lanes to a CU, and
+// an exponential and about ten more instructions per logit.  A single row is a chain of
+// latencies: load, two exchanges between waves, candidates, 10 us.
 #include <type_traits>
 
 #include "logprobs.h"
