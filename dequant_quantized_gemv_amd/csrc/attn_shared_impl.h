@@ -185,10 +185,17 @@ __device__ __forceinline__ void attn_prefix_block(const SharedArgs &a, const int
     };
 
     struct Quad { uint32_t k[4][2 * ES], v[4][2 * ES]; } reg[NU];
+    // Pieces of a row that neighbouring lanes read: eight where they divide it, whole
+    // lines of 128 bytes in fp16 (16 groups of 8 rows, head size 64, 60 us with four, 60 with
+    // eight that meet on the same banks in LDS, 52 with eight; 8 bits gain nothing).
+    constexpr int PIECES = std::min((D / 8) & -(D / 8), 8);
     auto unit_at = [&](int u, int &quad, int &piece) {
-        quad = (u >> 2) % NQ;
-        piece = 4 * ((u >> 2) / NQ) + (u & 3);
+        quad = (u / PIECES) % NQ;
+        piece = PIECES * (u / PIECES / NQ) + u % PIECES;
     };
+    // Where a dimension has the tokens at `pos` (every 16 dimensions in another
+    // order: eight neighbouring pieces would be stored to the same banks).
+    auto swizzled = [&](int dim, int pos) { return pos ^ (16 * (dim >> 4 & 3)); };
     auto load = [&](int n) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
@@ -233,7 +240,7 @@ __device__ __forceinline__ void attn_prefix_block(const SharedArgs &a, const int
                                                      d % 2 ? 0x07060302u : 0x05040100u);
                     }
                 }
-                *reinterpret_cast<u2_t *>(lds + L::kValues + (8 * piece + d) * L::kDim + 2 * pos) = w;
+                *reinterpret_cast<u2_t *>(lds + L::kValues + (8 * piece + d) * L::kDim + 2 * swizzled(8 * piece, pos)) = w;
             }
         }
     };
@@ -343,7 +350,7 @@ __device__ __forceinline__ void attn_prefix_block(const SharedArgs &a, const int
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int c2 = 0; c2 < DB; ++c2)
-                    vv[s][c2] = *reinterpret_cast<const u4_t *>(lds + L::kValues + (32 * c2 + j) * L::kDim + 2 * (b0 + 16 * s + 8 * g));
+                    vv[s][c2] = *reinterpret_cast<const u4_t *>(lds + L::kValues + (32 * c2 + j) * L::kDim + 2 * swizzled(32 * c2 + j, b0 + 16 * s + 8 * g));
             __builtin_amdgcn_sched_barrier(0);
             float p[16];
 #pragma unroll
