@@ -33,9 +33,9 @@
 // by its products).
 //
 // What bounds it: long shared parts their products (64 sequences of 4 x 8 heads of 128 over
-// 32768 tokens: 103 us, of it 92 in loops that reach 74 % of the matrix rate; each product
+// 32768 tokens: 101 us, of it 88 in loops that reach 77 % of the matrix rate; each product
 // is done twice for its second part), few rows the traffic (8 sequences over 32768
-// tokens 44 us, 3.1 TB/s; 1 x 128000 tokens of head size 64 5.1 TB/s), own tokens
+// tokens 43 us, 3.2 TB/s; 1 x 128000 tokens of head size 64 5.1 TB/s), own tokens
 // what bounds the decode kernel, before and not beside the rest: the registers
 // leave room for two workgroups to a CU.  Own tokens go first; shared ones first, or
 // one after the other in turn, took 64 x 32768 from 104 to 120 us.
