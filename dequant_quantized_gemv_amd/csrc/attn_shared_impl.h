@@ -33,9 +33,9 @@
 // by its products).
 //
 // What bounds it: long shared parts their products (64 sequences of 4 x 8 heads of 128 over
-// 32768 tokens: 101 us, of it 88 in loops that reach 77 % of the matrix rate; each product
-// is done twice for its second part), few rows the traffic (8 sequences over 32768
-// tokens 43 us, 3.2 TB/s; 1 x 128000 tokens of head size 64 5.1 TB/s), own tokens
+// 32768 tokens: 101 us, of which 66 grow with the tokens: 1.05 PFLOP/s with the second
+// parts; the rest is beginnings and ends, own tokens and the join), few rows the
+// traffic (8 sequences: 43 us, of which 22 grow with the tokens, 6.1 TB/s), own tokens
 // what bounds the decode kernel, before and not beside the rest: the registers
 // leave room for two workgroups to a CU.  Own tokens go first; shared ones first, or
 // one after the other in turn, took 64 x 32768 from 104 to 120 us.
