@@ -161,12 +161,14 @@ __device__ __forceinline__ void attn_prefix_block(const SharedArgs &a, const int
     const int left = rows - wrow;                      // of its 32
     const int row = wrow + min(j, max(left, 1) - 1);   // lane's (one that is there)
     const int member = row / a.group;
-    const int seq = first + min(member, rows / a.group - 1);
+    const int members = rows / a.group;
+    const int seq = first + min(member, members - 1);
     const int head = kvh * a.group + row - member * a.group;
 
     // places of the rows of a tile's tokens, one thread each; past the end
     // the last token's again
     const int32_t *table = a.table + first * a.ld_table;
+    const int first_len = *(const __attribute__((address_space(4))) int32_t *)(uintptr_t)(a.lens + first);
     uint32_t bad = 0;
     auto token_of = [&](int n) { return (int)min((int64_t)t0 + (int64_t)n * BN + tid, (int64_t)t1 - 1); };
     auto page_of = [&](int t) { return (int)((uint64_t)(uint32_t)t * a.page_magic >> a.page_shift); };
@@ -182,6 +184,20 @@ __device__ __forceinline__ void attn_prefix_block(const SharedArgs &a, const int
             sc[0] = a.ks[at];
             sc[1] = a.vs[at];
         }
+    };
+
+    // A first sequence that was dropped or cut short has ids outside the pool where
+    // its pages were: a chunk with such a page is read by the row of the first
+    // sequence that has all shared tokens (there is none: nobody has a result).
+    auto living = [&]() __attribute__((always_inline)) {
+        bool gone = false;
+        for (int p = page_of(t0) + lane; p <= page_of(t1 - 1); p += 64) gone = gone || (unsigned)table[p] >= (unsigned)a.n_pages;
+        if (!__any(gone)) return first;
+        for (int s = 0; s < members; s += 64) {
+            const uint64_t has = __ballot(s + lane < members && a.lens[first + min(s + lane, members - 1)] >= shared);
+            if (has != 0) return __builtin_amdgcn_readfirstlane(first + s + __builtin_ctzll(has));
+        }
+        return first;
     };
 
     struct Quad { uint32_t k[4][2 * ES], v[4][2 * ES]; } reg[NU];
@@ -253,10 +269,20 @@ __device__ __forceinline__ void attn_prefix_block(const SharedArgs &a, const int
         for (int s = 0; s < KS; ++s) __builtin_memcpy(qv[s], q + 16 * s, 32);
     }
     asm volatile("" ::: "memory");
-    int id = 0;
+    int p0 = 0, p1 = 0, id = 0;
+    auto first_pages = [&]() __attribute__((always_inline)) {
+        if (tid < BN) {
+            p0 = table[page_of(token_of(0))];
+            p1 = table[page_of(token_of(1))];
+            id = table[page_of(token_of(2))];
+        }
+    };
+    first_pages();
+    if (first_len < shared) {   // (asked for beside the length that tells whether the row has them)
+        table = a.table + living() * a.ld_table;
+        first_pages();
+    }
     if (tid < BN) {
-        const int p0 = table[page_of(token_of(0))], p1 = table[page_of(token_of(1))];
-        id = table[page_of(token_of(2))];
         place(0, p0, sc0);
         place(1, p1, sc1);
     }

@@ -979,7 +979,8 @@ def attn_decode_shared(cache, q, table, lens, starts, shared, scale=None, max_le
     """attn_decode for a batch in which groups of sequences share their first
     tokens, which are read once per group: group g is sequences starts[g] ..
     starts[g + 1] - 1, and each begins with the shared[g] tokens in the pages of
-    the first of them.  starts int32 (n_groups + 1,), ascending; shared int32
+    the first of them (or, where it has ended and kv_fork left -1 in its row, of
+    the first that has them all).  starts int32 (n_groups + 1,), ascending; shared int32
     (n_groups,).  max_shared and max_own bound shared and lens - shared (default:
     max_len) and size the split.  Other arguments and y as attn_decode."""
     import torch

@@ -540,9 +540,14 @@ size_t qk_attn_decode_workspace(const qk_kv_cache *cache, int64_t n_seqs, int64_
  *   group g: sequences starts[g] .. starts[g + 1] - 1, of which each begins with
  *   the shared[g] tokens that lie in the pages of the first of them
  *
- * The result is that of qk_attn_decode without a window, but for rounding:
- * of another sequence's table only entries of pages with tokens of its own, at or
- * behind shared[g], are followed.  Sequences of no group share nothing.
+ * The result is that of qk_attn_decode without a window, but for rounding.
+ * Shared tokens are read by the first sequence's row of the table, of which they need
+ * not be tokens still: it may have ended (dropped or cut short) and kept its row.  Where
+ * it has fewer tokens than are shared and entries of its row are outside the pool, as
+ * qk_kv_fork leaves it, they are read by the row of the first sequence of the group
+ * that has all of them.  Of the others' rows only entries of pages with
+ * tokens of their own, at or behind shared[g], are followed.  Sequences of no group
+ * share nothing.
  * lens[s] <= 0: zeros.  NaN: lens[s] above max_len or below shared[g], more
  * shared tokens than max_shared, more of its own than max_own, or a page id
  * outside the pool; and the whole batch where starts does not ascend within
