@@ -286,6 +286,7 @@ int shared_plan(const qk_kv_cache &c, int64_t n_seqs, int64_t n_q_heads, int64_t
     a.own_waves = alone ? 1 : qk::kAttnWaves;
     a.prefix_chunks = 0;
     a.prefix_tiles = 1;
+    a.row_waves = qk::prefix_tokens((int)c.head_dim) < 128 ? 2 : 1;   // (nothing shared: the fewest registers)
     if (n_groups > 0 && max_shared > 0) {
         const int64_t groups = std::min(n_groups, n_seqs);
         const int64_t each = (n_seqs * a.group + groups - 1) / groups;   // query rows of a group
