@@ -25,8 +25,9 @@
 // to head size 64: 32 groups of 16 rows there 28.2 -> 25.5, at 128 spilled, 44 -> 59).
 //
 // Scores as in the decode kernel: exact keys, q in two fp16 parts.  The low
-// part is never 0 beside a high part that is not, so that a key which
-// overflowed to infinity keeps its sign.  Probabilities: with 8-bit values
+// part is never 0 beside a high part that is not (fp16's least value is added to
+// it, 2^-37 of the row's largest), so that a key which overflowed to infinity
+// keeps its sign.  Probabilities: with 8-bit values
 // all 24 bits in three bf16 parts; with fp16 values two fp16 parts of 2^12 p,
 // which holds p within 2^-21 of itself and 2^-36 of the row's largest (the exact form,
 // v_mfma_f32_16x16x4_f32, has an eighth of the rate, and this kernel is bound
@@ -311,12 +312,12 @@ __device__ __forceinline__ void attn_prefix_block(const SharedArgs &a, const int
             for (int i = 0; i < 8; ++i) qv[s][i] = ldexpf(qv[s][i], -qexp);
             split8(qv[s], qh[s], ql[s]);
             if constexpr (!I8) {
-                // (2^-14 of the high part's sign is added where that is not 0: 2^-27 of the
-                // row's largest; the low part has the same sign or is 0)
+                // (fp16's least value with the high part's sign is added where that is not 0:
+                // 2^-37 of the row's largest; the low part has the same sign or is 0)
                 typedef uint16_t s8_t __attribute__((ext_vector_type(8)));
                 const s8_t h = __builtin_bit_cast(s8_t, qh[s]);
                 const s8_t some = __builtin_elementwise_min((s8_t)(h & (uint16_t)0x7FFF), (s8_t)(uint16_t)1);
-                ql[s] += __builtin_bit_cast(h8_t, (s8_t)(some * (uint16_t)0x0400 | (h & (uint16_t)0x8000)));
+                ql[s] += __builtin_bit_cast(h8_t, (s8_t)(some | (h & (uint16_t)0x8000)));
             }
         }
         if constexpr (I8) qexp += 9;  // codes are held times 2^-9
