@@ -837,7 +837,9 @@ def moe_route(logits, n_used, score="softmax", bias=None, n_groups=1, topk_group
 # Sequences that share pages, and what their answers are chosen by.
 
 def _scratch(workspace, need, device):
-    """The caller's workspace, or one of its own where one is needed."""
+    """The caller's workspace, or one of its own where one is needed.  The
+    caller of this holds it until the library has taken the call: a block that
+    went back to its pool before could be given to another thread."""
     import torch
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=device) if need else None
@@ -925,7 +927,8 @@ def kv_fork(table, lens, new_lens, page_size, n_pages, parent=None, out=None, wo
         ld_out = out.stride(0)
     src, dst, missing = table.new_empty(n), table.new_empty(n), table.new_empty(1)
     _on_device(table, lens, new_lens, parent, out, workspace)
-    work, size = _ptr_bytes(_scratch(workspace, 0 if workspace is not None else qk_kv_pages_workspace(n, n_pages), table.device))
+    workspace = _scratch(workspace, 0 if workspace is not None else qk_kv_pages_workspace(n, n_pages), table.device)
+    work, size = _ptr_bytes(workspace)
     st = load().qk_kv_fork(table.data_ptr(), table.stride(0), lens.data_ptr(), rows, pages,
                            parent.data_ptr() if parent is not None else None, new_lens.data_ptr(), n, out.shape[1],
                            page_size, n_pages, out.data_ptr(), ld_out, src.data_ptr(), dst.data_ptr(),
@@ -955,8 +958,8 @@ def kv_compact(table, lens, page_size, n_pages, out=None, workspace=None, stream
     n = n_pages // 2
     src, dst, live = table.new_empty(n), table.new_empty(n), table.new_empty(1)
     _on_device(table, lens, out, workspace)
-    work, size = _ptr_bytes(_scratch(workspace, 0 if workspace is not None else qk_kv_pages_workspace(table.shape[0], n_pages),
-                                     table.device))
+    workspace = _scratch(workspace, 0 if workspace is not None else qk_kv_pages_workspace(rows, n_pages), table.device)
+    work, size = _ptr_bytes(workspace)
     st = load().qk_kv_compact(table.data_ptr(), table.stride(0), lens.data_ptr(), rows, pages,
                               page_size, n_pages, out.data_ptr(), out.stride(0), src.data_ptr(), dst.data_ptr(),
                               live.data_ptr(), work, size, _stream_of(table))
@@ -1018,7 +1021,8 @@ def attn_decode_shared(cache, q, table, lens, starts, shared, scale=None, max_le
         _heads_check(y, "y", dt, n, heads, dim)
     _on_device(cache.k, q, table, lens, starts, shared, y, workspace)
     need = 0 if workspace is not None else qk_attn_decode_shared_workspace(cache.desc, n, heads, max_len, max_shared, max_own)
-    work, size = _ptr_bytes(_scratch(workspace, need, q.device))
+    workspace = _scratch(workspace, need, q.device)
+    work, size = _ptr_bytes(workspace)
     q_head, y_head = (q.stride(1), y.stride(1)) if heads > 1 else (0, 0)
     st = load().qk_attn_decode_shared(cache.desc, q.data_ptr(), _row_stride(q), q_head, n, heads, table.data_ptr(),
                                       table.stride(0), lens.data_ptr(), max_len, starts.data_ptr(), shared.data_ptr(),
@@ -1078,8 +1082,8 @@ def token_logprobs(logits, ids=None, top=0, scale=1.0, workspace=None, stream=No
     if top:
         best_ids = logits.new_empty((n, top), dtype=torch.int32)
     _on_device(logits, ids, workspace)
-    work, size = _ptr_bytes(_scratch(workspace, 0 if workspace is not None else qk_token_logprobs_workspace(n, vocab, top),
-                                     logits.device))
+    workspace = _scratch(workspace, 0 if workspace is not None else qk_token_logprobs_workspace(n, vocab, top), logits.device)
+    work, size = _ptr_bytes(workspace)
     st = load().qk_token_logprobs(QK_F32 if dtype is torch.float32 else QK_F16, logits.data_ptr(), logits.stride(0), n,
                                   vocab, scale, ip, ld_ids, m, lp.data_ptr() if lp is not None else None, m,
                                   entropy.data_ptr(), top, best_ids.data_ptr() if top else None, top,
