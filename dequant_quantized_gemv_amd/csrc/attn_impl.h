@@ -153,18 +153,18 @@ __device__ __forceinline__ int shared_tokens(const SharedArgs &a, int seq, int l
     return fine ? shared : -1;
 }
 
-// TILED: a page holds whole sub-tiles (page_size a multiple of 16) and scales
-// of neighbouring tokens lie side by side, so a sub-tile's page is looked up
-// once, in scalar registers.  Otherwise lane l finds the row (and reads the
-// scales) of the tile's token l % 32, and lanes take them from one another.
-// With SharedArgs the tokens that a sequence has of its own, behind those that
-// its group shares, always to partial results.
 // A workgroup's results on the way to one another: maximum and sum, outputs.
 typedef float AttnWaveSums[kAttnWaves][kAttnHeads][2];
 template <int D> using AttnWaveOutputs = float[kAttnWaves][kAttnHeads][D + 4];
 
 // Workgroup `block` of `blocks`, or, where the wave takes a sequence's own tokens
 // alone, four of `blocks`.
+// TILED: a page holds whole sub-tiles (page_size a multiple of 16) and scales
+// of neighbouring tokens lie side by side, so a sub-tile's page is looked up
+// once, in scalar registers.  Otherwise lane l finds the row (and reads the
+// scales) of the tile's token l % 32, and lanes take them from one another.
+// With SharedArgs the tokens that a sequence has of its own, behind those that
+// its group shares, always to partial results.
 template <int D, bool I8, bool TILED, class ARGS>
 __device__ __forceinline__ void attn_decode_block(const ARGS &a, const int block, const int blocks, AttnWaveSums &sm, AttnWaveOutputs<D> &so) {
     constexpr bool SHARED = std::is_same_v<ARGS, SharedArgs>;

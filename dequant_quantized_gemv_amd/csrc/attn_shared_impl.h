@@ -37,9 +37,19 @@
 // 32768 tokens: 101 us, of which 66 grow with the tokens: 1.05 PFLOP/s with the second
 // parts; the rest is beginnings and ends, own tokens and the join), few rows the
 // traffic (8 sequences: 43 us, of which 22 grow with the tokens, 6.1 TB/s), own tokens
-// what bounds the decode kernel, before and not beside the rest: the registers
-// leave room for two workgroups to a CU.  Own tokens go first; shared ones first, or
-// one after the other in turn, took 64 x 32768 from 104 to 120 us.
+// what bounds the decode kernel, before and not beside the rest: from head size 96 up (and
+// with 64 or more rows at 64) the registers leave room for two workgroups to a CU, below
+// that for three.  Own tokens go first; shared ones first, or
+// one after the other in turn, took 64 x 32768 from 104 to 120 us.  8 bits spend more
+// vector instructions than products (12 to a product against 6 in fp16, to make fp16
+// keys, bf16 values and three parts of the probabilities); at head size 128 4 (64 rows) to
+// 7 (128) registers are spilled, outside the loop.  Above 128 q's parts and
+// the outputs fill the 256 vector registers, and the loop moves others to and from the
+// accumulation registers (at 256 2.6 moves to a product; 64 sequences of 2 x 8 heads of 256
+// over 16384 tokens 71 us where their products are 31).
+// Groups are found by looking through all of them, 64 at a time, in every workgroup: up to
+// 64 it is one step, 1024 groups of 2 sequences behind 512 tokens take 776 us where the decode
+// kernel takes 645, 4096 sequences of groups of their own 1540 against 219.
 #pragma once
 
 #include "attn_impl.h"
@@ -643,7 +653,8 @@ int attn_shared_dim(const SharedArgs &a, bool tiled, hipStream_t stream) {
     else if constexpr (prefix_tokens(D) == 128) st = attn_shared_tiled<D, I8, 1>(a, tiled, stream);
     else return QK_ERR_INVALID_ARG;
     // A wave joins a row of few partial results where there are many rows, four
-    // waves otherwise (8192 rows of 9 23 / 16 us with four / one, 2048 rows of 33 10 / 11).
+    // waves otherwise (8192 rows of 9 23 / 16 us with four / one, 2048 rows of 33 10 / 11;
+    // the whole call with 2048 rows of 17 66.6 / 68.3).
     const bool one_wave = a.slots <= 16 && (int64_t)a.n_seqs * a.n_heads >= 1024;
     const int64_t most = max_groups(256) / a.n_heads;  // sequences of one launch
     for (int64_t i = 0; i < a.n_seqs && st == QK_OK; i += most) {

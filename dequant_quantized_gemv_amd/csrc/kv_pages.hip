@@ -9,9 +9,11 @@
 // pages, and over the requests in the order of rows), never from the order in
 // which atomics arrive.
 //
-// What bounds them: a large copy its traffic (2000 pages of 128 KB, 236 MB read and
-// written, 47 us or 5.0 TB/s; over sets of pages that the Infinity Cache holds 41), a
-// small one its launch and two dependent loads (8 pages of 34 KB 2.5 us).  Tables are
+// What bounds them: a large copy its traffic (a list of 2000 pages of 64 KB of which 1800
+// are copied, 236 MB read and written together, 47 us or 5.0 TB/s; 41 where the Infinity
+// Cache holds a part of them from the call before), a small one its launch and two
+// dependent loads (8 pages of 34 KB 2.5 us), a long list of few moves the workgroups that
+// find nothing to do (100 moves in a list of 32768 65 us, in one of 100 3.5).  Tables are
 // small and their work is a chain of passes that each wait for the one before
 // (rows, bits, ranks, places): one workgroup's latency, 5.9 us for 4 rows of
 // 63 pages, 13.1 for 64 rows of 256 (16384 entries through one CU); to pack, 7.1
@@ -48,8 +50,8 @@ __device__ __forceinline__ int64_t run_offset(const CopyPlane &p, int64_t at) {
 
 constexpr int kCopyStep = kCopyThreads * kCopyUnroll;   // pieces of a workgroup
 
-// STREAM: with stores that leave the caches alone (2000 pages of 128 KB 57 -> 43 us,
-// 262 MB; no difference where the pages fit the caches).
+// STREAM: with stores that leave the caches alone (2000 pages of 64 KB 57 -> 43 us,
+// 262 MB read and written together; no difference where the pages fit the caches).
 template <typename PIECE, bool STREAM>
 __device__ __forceinline__ void copy_chunk(const CopyPlane &p, int src, int dst, int64_t chunk) {
     PIECE x[kCopyUnroll];
@@ -273,8 +275,11 @@ __global__ __launch_bounds__(256) void fork_write_kernel(const ForkArgs a) {
 }
 
 // Tables and pools up to these sizes are planned by one workgroup, the bits in
-// LDS: one launch instead of four (fork of 4 rows of 63 pages
-// 11.5 -> 5.7 us, 64 of 256 19 -> 13).
+// LDS: one launch instead of four.  In us with one / four, each row's last page
+// copied: fork of 4 rows of 63 pages 5.7 / 11.5, 64 of 256 13 / 19, 1024 of 16 16 / 29,
+// 1024 of 64 41 / 44, 256 of 256 38 / 33, 64 of 1024 37 / 26; each row grown in its place
+// 64 of 256 11 / 14, 64 of 1024 33 / 18; packed 64 of 256 11 / 14, 64 of 1024 17 / 16.  So
+// forks of few long rows are quicker in four launches from about 30000 entries on.
 constexpr int kOneRows = 1024, kOneList = 4096;
 constexpr int64_t kOnePages = 1 << 18, kOneEntries = 1 << 16;
 

@@ -13,10 +13,13 @@
 // they do not hang on the order in which anything arrives.
 //
 // Many rows are bound by reading the logits once: 2048 of 32000 in fp32 51 us without
-// the best (262 MB, 5.1 TB/s), 54 with 5 of them, 66 with 64.  In fp16 46, which is
-// half the bytes and the same instructions: one workgroup of 1024 lanes to a CU, and
-// an exponential and about ten more instructions per logit.  A single row is a chain of
-// latencies: load, two exchanges between waves, candidates, 10 us.
+// the best (262 MB, 5.1 TB/s), 54 with 5 of them, 66 with 64.  In fp16 44, which is
+// half the bytes and the same instructions: 22 a logit with everything, 22 million of
+// the waves', which are 36 us of four cycles each on 1024 SIMDs (two workgroups of
+// 1024 lanes share a CU, so one's loads meet the other's sums).  A row of more than 32768
+// logits takes a second launch (512 x 131072 in fp32 with 5 best 59 us, 4.6 TB/s; 64 x 131072
+// with 20 best 20).  A single row is a chain of latencies: load, two exchanges between
+// waves, candidates, 10 us.
 #include <type_traits>
 
 #include "logprobs.h"
@@ -82,7 +85,6 @@ struct Stat {
     double equal, s, w;
 };
 
-// Writes a row's results: a.lp, a.entropy and the best from their orders.
 // The i-th token asked for (-1 behind the last) and its logit.
 __device__ __forceinline__ int asked_id(const LogpArgs &a, int64_t row, int i) {
     return i < a.n_ids ? a.ids[row * a.ld_ids + i] : -1;
@@ -92,6 +94,7 @@ __device__ __forceinline__ float asked_logit(const LogpArgs &a, int64_t row, boo
     return f16 ? h2f(static_cast<const uint16_t *>(a.x)[row * a.ldx + id]) : static_cast<const float *>(a.x)[row * a.ldx + id];
 }
 
+// Writes a row's results: a.lp, a.entropy and the best from their orders.
 __device__ __forceinline__ void write_row(const LogpArgs &a, int64_t row, const Stat &t, float asked, bool f16,
                                           const uint64_t *best, int threads) {
     const double rest = t.equal - 1.0 + t.s;   // S - 1

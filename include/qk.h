@@ -561,7 +561,9 @@ size_t qk_attn_decode_workspace(const qk_kv_cache *cache, int64_t n_seqs, int64_
  * give NaN.
  *
  *   starts, shared   device int32[n_groups + 1] and int32[n_groups]; n_groups
- *              >= 0 (NULL with 0)
+ *              >= 0 (NULL with 0).  Every part of the work looks through all
+ *              groups, which costs little up to a few hundred; thousands of small
+ *              ones are quicker in qk_attn_decode
  *   max_len    1..2^30, no length is above it
  *   max_shared, max_own   0..max_len and 1..max_len: bounds of shared[g] and of
  *              lens[s] - shared[g]; the parts are sized for them
